@@ -203,6 +203,66 @@ moe_status nvfp4_quantize_block16(const void* in, long long rows, int cols, long
 moe_status moe_route_topk(const moe_plan* plan, const float* logits, const int* live_count_dev,
                           int* ids, float* probs, void* stream);
 
+/* Training the router: a balance loss that keeps the experts evenly used, a z
+ * loss that keeps the logits small, per-expert route counts, and the gradient of
+ * the logits.  They stand beside moe_route_topk (no counterpart in the pages: an
+ * addition of this library).
+ *
+ * Which tokens count: the live rows that lie in a sequence, whose mask byte is
+ * not 0 and whose logits are not all -infinity; T_s of them in sequence s, T in
+ * all, S' the number of sequences with T_s > 0.  With p_t = softmax(logits[t])
+ * and lse_t = log(sum(exp(logits[t]))):
+ *   counts      int32 [num_seqs, E]: routes of the counted tokens of s to e.
+ *               Ids outside [0, E) (dropped routes) are not counted.
+ *   prob_sums   fp32 [num_seqs, E]: sum of p_t[e] over the counted tokens of s.
+ *   lse         fp32 [capacity]: lse_t; -infinity for a live token that does not
+ *               count; rows >= the live count are not written.
+ *   losses      fp32 [2]:
+ *     [0] balance: balance_coef * the mean over the S' sequences of
+ *         E * sum_e (counts[s,e] / (k T_s)) * (prob_sums[s,e] / T_s)
+ *     [1] z: z_coef * the mean over the T tokens of lse_t^2
+ *     Both are 0 when no token counts.
+ *   grad_scales fp32 [num_seqs + 1]: what moe_route_backward multiplies by:
+ *               balance_coef * E / (S' k T_s^2) for each s (0 where T_s = 0), then
+ *               2 z_coef / T (0 where T = 0).
+ * Inputs: logits fp32 [capacity, E]; ids int32 [capacity, k] in any order;
+ * token_mask uint8 [capacity] or NULL (all ones): rows whose byte is 0 are not
+ * read; seq_offsets int32 [num_seqs + 1], nondecreasing: sequence s is the live
+ * rows [seq_offsets[s], seq_offsets[s+1]) (bounds past the live count are clamped
+ * to it; sequences may be empty), or NULL with num_seqs 1 for all live rows.
+ * num_seqs: 1 .. MOE_MAX_SEQS.  A NaN or +infinity among a counted token's logits
+ * makes the losses and its expert sums NaN.  Sums are held in fp32 and added in a
+ * fixed order: the same inputs give the same bits.  workspace:
+ * moe_balance_workspace_bytes(plan, num_seqs), 256-byte aligned; nothing in it
+ * outlives the call.  Enqueues work only. */
+#define MOE_MAX_SEQS 65536
+size_t moe_balance_workspace_bytes(const moe_plan* plan, int num_seqs);
+moe_status moe_balance_loss(const moe_plan* plan, const float* logits, const int* ids, const uint8_t* token_mask,
+                            const int* seq_offsets, int num_seqs, float balance_coef, float z_coef,
+                            const int* live_count_dev, int* counts, float* prob_sums, float* lse, float* losses,
+                            float* grad_scales, void* workspace, size_t ws_bytes, void* stream);
+
+/* Gradient of the logits: dlogits fp32 [capacity, E], every live row written
+ * whole (rows >= the live count are not written), the sum of
+ *   - the losses' part (counts, grad_scales, lse and logits given, all as
+ *     moe_balance_loss left them; counts are constants of it):
+ *       p_t[e] * (g[0] grad_scales[s] (counts[s,e] - sum_i counts[s,i] p_t[i])
+ *                 + g[1] grad_scales[num_seqs] lse_t)
+ *     with g = grad_losses fp32 [2] on the device, or 1 and 1 when NULL;
+ *   - the chosen part (ids, probs and dprobs given): probs[t, j] are the chosen
+ *     experts' renormalised probabilities (moe_route_topk) and dprobs[t, j] their
+ *     gradients (moe_combine_backward), in the order of ids:
+ *       probs[t,j] * (dprobs[t,j] - sum_i probs[t,i] dprobs[t,i])
+ *     added at column ids[t, j]; routes with an id outside [0, E) are left out of
+ *     both sums, and an id that stands twice gets both.
+ * Either part may be absent (its pointers NULL), not both.  A token that does not
+ * count (lse -infinity) gets a row of zeros; without lse every live token counts.
+ * seq_offsets, num_seqs: as given to moe_balance_loss.  Enqueues work only. */
+moe_status moe_route_backward(const moe_plan* plan, const float* logits, const int* ids, const float* lse,
+                              const int* counts, const float* grad_scales, const float* grad_losses,
+                              const float* probs, const float* dprobs, const int* seq_offsets, int num_seqs,
+                              const int* live_count_dev, float* dlogits, void* stream);
+
 /* The routed SwiGLU expert forward.
  *   x        bf16 [capacity, H]: token rows; only rows < live count are read.
  *   logits   fp32 [capacity, E] or NULL: routed here as moe_route_topk does;
@@ -342,6 +402,25 @@ moe_status moe_ep_dispatch(const moe_plan* plan, int ep_size, const void* x, con
 moe_status moe_ep_combine(const moe_plan* plan, const float* y_rows, const int* route_rows,
                           const float* route_probs, const int* live_count_dev, void* out, void* stream);
 
+/* Gradient of the combine: of moe_forward's (its y rows and their places are
+ * the workspace views y and inv, its probabilities route_probs) and of
+ * moe_ep_combine's (the same arguments).  dout: the gradient of out, in out's
+ * type (fp32, or bf16 under MOE_FLAG_OUT_BF16) [capacity, H], 16-byte aligned.
+ * For each live token t and route j, with r = route_rows[t, j]:
+ *   dprobs   fp32 [capacity, k]: dprobs[t, j] = <dout[t], y_rows[r]>, summed in
+ *            fp32 in an order fixed by H alone; 0 where r < 0 (a dropped
+ *            route).  May be NULL (y_rows is then not read and may be NULL).
+ *   dy_rows  fp32 [rows, H], 16-byte aligned: row r = route_probs[t, j] *
+ *            dout[t]; rows that no live route names are not written.  May be
+ *            NULL, but not together with dprobs.
+ * Rows >= the live count are not read or written.  route_rows must name every
+ * row once, as the combine's do.  Under MOE_FLAG_PROBS_IN_FC1 the combine's
+ * weights are 1: pass them as route_probs, and take dprobs for the gradient of
+ * those weights, not of the router's probabilities.  Enqueues work only. */
+moe_status moe_combine_backward(const moe_plan* plan, const void* dout, const float* y_rows, const int* route_rows,
+                                const float* route_probs, const int* live_count_dev, float* dprobs, float* dy_rows,
+                                void* stream);
+
 /* Expert-parallel exchange through peer memory (no counterpart to call in
  * the pages, which put the EP transport inside their expert kernels:
  * Megatron-LM PR #7830; the NCCL all-to-all of steps 2 and 4 above reads the
@@ -456,6 +535,8 @@ typedef struct {
     const float* xq_row_scales;
     const float* h_row_scales;
     const float* h_fp32;
+    const float* y;         /* fp32 [rows_padded, H]: the down GEMM's rows, row inv[t, j]
+                               the output of route (t, j) before the combine          */
 } moe_workspace_views;
 moe_status moe_get_workspace_views(const moe_plan* plan, const void* workspace,
                                    moe_workspace_views* views);

@@ -26,7 +26,8 @@ __all__ = [
     "MoeError", "Plan", "load_library", "library_path", "moe_version", "moe_plan_create", "moe_plan_destroy",
     "moe_weight_buffer_bytes", "moe_workspace_bytes", "alloc_weight_buffer", "alloc_workspace",
     "moe_prepare_weights", "mxfp8_quantize_block32", "nvfp4_quantize_block16", "moe_route_topk", "moe_forward",
-    "moe_forward_with_events",
+    "moe_forward_with_events", "moe_balance_workspace_bytes", "moe_balance_loss", "moe_route_backward",
+    "moe_combine_backward", "MOE_MAX_SEQS",
     "moe_forward_noalloc", "MOE_NOALLOC_SCRATCH_BYTES", "moe_ep_dispatch", "moe_ep_combine",
     "MOE_NUM_STAGES", "STAGE_NAMES",
     "moe_get_workspace_views", "moe_get_device_status", "moe_clear_device_status",
@@ -70,7 +71,7 @@ class _Views(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("route_ids", "route_probs", "offsets", "perm", "inv", "pad_offsets",
                                                  "h", "h_scales", "xq", "xq_scales")] + [
         ("rows_padded", ctypes.c_longlong), ("status", ctypes.c_void_p), ("xq_row_scales", ctypes.c_void_p),
-        ("h_row_scales", ctypes.c_void_p), ("h_fp32", ctypes.c_void_p)]
+        ("h_row_scales", ctypes.c_void_p), ("h_fp32", ctypes.c_void_p), ("y", ctypes.c_void_p)]
 
 
 _lib = None
@@ -85,7 +86,7 @@ def load_library():
         raise RuntimeError(f"routed_moe_swiglu_b200: CUDA library not built ({library_path} missing); "
                            "run `python -m routed_moe_swiglu_b200.build`")
     lib = ctypes.CDLL(library_path)
-    P, I, LL, SZ = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t
+    P, I, LL, SZ, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong, ctypes.c_size_t, ctypes.c_float
     sig = {
         "moe_plan_create": ([ctypes.POINTER(_Desc), ctypes.POINTER(P)], I),
         "moe_plan_destroy": ([P], None),
@@ -96,6 +97,10 @@ def load_library():
         "mxfp8_quantize_block32": ([P, LL, I, LL, P, P, P, P], I),
         "nvfp4_quantize_block16": ([P, LL, I, LL, P, P, P, P, P], I),
         "moe_route_topk": ([P, P, P, P, P, P], I),
+        "moe_balance_workspace_bytes": ([P, I], SZ),
+        "moe_balance_loss": ([P, P, P, P, P, I, F, F, P, P, P, P, P, P, P, SZ, P], I),
+        "moe_route_backward": ([P, P, P, P, P, P, P, P, P, P, I, P, P, P], I),
+        "moe_combine_backward": ([P, P, P, P, P, P, P, P, P], I),
         "moe_forward": ([P, P, P, P, P, P, P, P, P, SZ, P], I),
         "moe_forward_with_events": ([P, P, P, P, P, P, P, P, P, SZ, P, ctypes.POINTER(P)], I),
         "moe_forward_noalloc": ([P, P, P, P, P, P, P, P, P], I),
@@ -266,6 +271,100 @@ def nvfp4_quantize_block16(x, q, scales, row_scales, live_rows=None, stream=None
 def moe_route_topk(plan: Plan, logits, live_count, ids, probs, stream=None) -> None:
     _check(load_library().moe_route_topk(plan.handle, _ptr(logits), _ptr(live_count), _ptr(ids), _ptr(probs),
                                          _stream(stream)), "moe_route_topk")
+
+
+MOE_MAX_SEQS = 65536
+
+
+def _dense(name: str, t, dtype: str, shape=None, rows=None, cols=None) -> None:
+    """`t` (or None) must be dense, of the dtype named and of `shape`; or, with `rows` and `cols`,
+    of any number of rows from `rows` on and of `cols` columns."""
+    if t is None:
+        return
+    import torch
+
+    if t.dtype is not getattr(torch, dtype):
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    got = tuple(t.shape)
+    if (shape is not None and got != shape) or (
+            rows is not None and (len(got) != 2 or got[0] < rows or got[1] != cols)):
+        raise ValueError(f"{name} must have shape {shape or (rows, cols)}, not {got}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def moe_balance_workspace_bytes(plan: Plan, num_seqs: int = 1) -> int:
+    return int(load_library().moe_balance_workspace_bytes(plan.handle, int(num_seqs)))
+
+
+def moe_balance_loss(plan: Plan, logits, ids, live_count, counts, prob_sums, lse, losses, grad_scales, workspace,
+                     balance_coef: float, z_coef: float = 0.0, token_mask=None, seq_offsets=None, stream=None) -> None:
+    """The router's balance and z losses with per-expert counts (include/moe.h).  The number of
+    sequences is counts.shape[0]; outputs: counts int32 and prob_sums fp32 [num_seqs, E], lse fp32
+    [capacity], losses fp32 [2] (balance, z), grad_scales fp32 [num_seqs + 1] (for moe_route_backward)."""
+    S, E, k, n = counts.shape[0], plan.num_experts, plan.top_k, plan.max_live_rows
+    _dense("logits", logits, "float32", rows=n, cols=E)
+    _dense("ids", ids, "int32", rows=n, cols=k)
+    _dense("live_count", live_count, "int32")
+    _dense("counts", counts, "int32", (S, E))
+    _dense("prob_sums", prob_sums, "float32", (S, E))
+    _dense("lse", lse, "float32")
+    if lse.numel() < n or (token_mask is not None and token_mask.numel() < n):
+        raise ValueError(f"lse and token_mask must have an element for each of the {n} rows")
+    _dense("losses", losses, "float32", (2,))
+    _dense("grad_scales", grad_scales, "float32", (S + 1,))
+    _dense("token_mask", token_mask, "uint8")
+    _dense("seq_offsets", seq_offsets, "int32", (S + 1,))
+    _check(load_library().moe_balance_loss(plan.handle, _ptr(logits), _ptr(ids), _ptr(token_mask), _ptr(seq_offsets), S,
+                                           float(balance_coef), float(z_coef), _ptr(live_count), _ptr(counts),
+                                           _ptr(prob_sums), _ptr(lse), _ptr(losses), _ptr(grad_scales),
+                                           _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                           _stream(stream)), "moe_balance_loss")
+
+
+def moe_route_backward(plan: Plan, logits, ids, live_count, dlogits, lse=None, counts=None, grad_scales=None,
+                       grad_losses=None, probs=None, dprobs=None, seq_offsets=None, stream=None) -> None:
+    """Gradient of the router's logits (include/moe.h): the losses' part from logits, lse, counts and
+    grad_scales (as moe_balance_loss left them) and grad_losses fp32 [2] (None: 1, 1); the chosen
+    part from ids, probs and dprobs.  Either part may be None."""
+    E, k, n = plan.num_experts, plan.top_k, plan.max_live_rows
+    S = counts.shape[0] if counts is not None else 1
+    _dense("logits", logits, "float32", rows=n, cols=E)
+    _dense("ids", ids, "int32", rows=n, cols=k)
+    _dense("live_count", live_count, "int32")
+    _dense("dlogits", dlogits, "float32", rows=n, cols=E)
+    _dense("lse", lse, "float32")
+    if lse is not None and lse.numel() < n:
+        raise ValueError(f"lse must have an element for each of the {n} rows")
+    _dense("counts", counts, "int32", (S, E))
+    _dense("grad_scales", grad_scales, "float32", (S + 1,))
+    _dense("grad_losses", grad_losses, "float32", (2,))
+    _dense("probs", probs, "float32", rows=n, cols=k)
+    _dense("dprobs", dprobs, "float32", rows=n, cols=k)
+    if counts is None:
+        seq_offsets = None  # the chosen part knows no sequences
+    _dense("seq_offsets", seq_offsets, "int32", (S + 1,))
+    _check(load_library().moe_route_backward(plan.handle, _ptr(logits), _ptr(ids), _ptr(lse), _ptr(counts),
+                                             _ptr(grad_scales), _ptr(grad_losses), _ptr(probs), _ptr(dprobs),
+                                             _ptr(seq_offsets), S, _ptr(live_count), _ptr(dlogits), _stream(stream)),
+           "moe_route_backward")
+
+
+def moe_combine_backward(plan: Plan, dout, y_rows, route_rows, route_probs, live_count, dprobs=None, dy_rows=None,
+                         stream=None) -> None:
+    """Gradient of the combine (include/moe.h): dprobs[t, j] = <dout[t], y_rows[route_rows[t, j]]> and
+    dy_rows[route_rows[t, j]] = route_probs[t, j] * dout[t]; either may be None."""
+    H, k, n = plan.hidden, plan.top_k, plan.max_live_rows
+    _dense("dout", dout, "bfloat16" if plan.out_dtype == "bf16" else "float32", rows=n, cols=H)
+    _dense("y_rows", y_rows, "float32", rows=0, cols=H)
+    _dense("route_rows", route_rows, "int32", rows=n, cols=k)
+    _dense("route_probs", route_probs, "float32", rows=n, cols=k)
+    _dense("live_count", live_count, "int32")
+    _dense("dprobs", dprobs, "float32", rows=n, cols=k)
+    _dense("dy_rows", dy_rows, "float32", rows=0, cols=H)
+    _check(load_library().moe_combine_backward(plan.handle, _ptr(dout), _ptr(y_rows), _ptr(route_rows),
+                                               _ptr(route_probs), _ptr(live_count), _ptr(dprobs), _ptr(dy_rows),
+                                               _stream(stream)), "moe_combine_backward")
 
 
 def _check_out(plan: Plan, out) -> None:

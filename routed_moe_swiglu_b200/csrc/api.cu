@@ -714,6 +714,7 @@ moe_status moe_get_workspace_views(const moe_plan* plan, const void* workspace, 
     v->xq_row_scales = fp4 ? reinterpret_cast<const float*>(ws + L.xg) : nullptr;
     v->h_row_scales = fp4 ? reinterpret_cast<const float*>(ws + L.hg) : nullptr;
     v->h_fp32 = L.hf != 0 ? reinterpret_cast<const float*>(ws + L.hf) : nullptr;
+    v->y = reinterpret_cast<const float*>(ws + L.y);
     v->rows_padded = plan->rows_pad;
     v->status = reinterpret_cast<const unsigned*>(ws + L.status);
     return MOE_OK;
