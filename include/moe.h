@@ -71,7 +71,7 @@ typedef enum {
     MOE_ERR_NOT_PREPARED = 6          /* reserved: weight buffer not prepared    */
 } moe_status;
 
-typedef enum { MOE_BF16 = 0, MOE_MXFP8 = 1, MOE_NVFP4 = 2 } moe_precision;
+typedef enum { MOE_BF16 = 0, MOE_MXFP8 = 1, MOE_NVFP4 = 2, MOE_INT8 = 3 } moe_precision;
 
 /* Device status bits (sticky until moe_clear_device_status). */
 #define MOE_DEV_LIVE_CLAMPED 0x1u  /* live count < 0 or > max live rows: clamped    */
@@ -91,7 +91,7 @@ typedef struct {
     long long max_live_rows; /* largest live count a call will pass (<= capacity);
                                 0 means capacity.  The workspace is sized for it;
                                 larger live counts are clamped and flagged.       */
-    moe_precision precision; /* MOE_BF16, MOE_MXFP8 or MOE_NVFP4                  */
+    moe_precision precision; /* MOE_BF16, MOE_MXFP8, MOE_NVFP4 or MOE_INT8        */
     unsigned flags;          /* MOE_FLAG_* variants; 0 for the plain forward      */
     float gate_up_clamp;     /* > 0: gate and up pre-activations clamped to
                                 [-gate_up_clamp, gate_up_clamp] before SwiGLU
@@ -119,15 +119,15 @@ typedef struct {
  *       [rows_padded, ceil(F/128)*128], into the workspace (the h_fp32
  *       view).  The workspace grows by that buffer and every h element costs
  *       one more 4-byte store; results are unchanged.  NVFP4 plans keep
- *       these rows always (its quantisation pass reads them); bf16 plans
- *       reject the flag. */
+ *       these rows always (its quantisation pass reads them); bf16 and
+ *       int8 plans reject the flag. */
 #define MOE_FLAG_KEEP_H_FP32 0x8u
 
 typedef struct moe_plan moe_plan; /* opaque, host memory only */
 
 /* Validate `desc` and build a host-side plan (no device work, no device
  * allocation).  Rejected (MOE_ERR_UNSUPPORTED): H or F not a multiple of 8
- * (bf16) or of 32 (MXFP8, NVFP4); k < 1, k > 16 or k > E; E < 1 or E > 1024;
+ * (bf16, int8) or of 32 (MXFP8, NVFP4); k < 1, k > 16 or k > E; E < 1 or E > 1024;
  * capacity < 1 or > 2^24 rows; max_live_rows < 0 or > capacity;
  * H > 16384 or F > 16384.  Rejected (MOE_ERR_INVALID_ARG): unknown flag
  * bits, a negative or non-finite gate_up_clamp. */
@@ -153,7 +153,9 @@ size_t moe_workspace_bytes(const moe_plan* plan);
  * In MXFP8 the weights are quantised here (blocks of 32 along each GEMM's K:
  * H for gate/up, F for down); in NVFP4 likewise (blocks of 16) with one
  * second-level scale per expert matrix (W1 = gate and up together, W2), as
- * nvfp4_quantize_block16 describes.  Enqueued on `stream`; forwards enqueued later
+ * nvfp4_quantize_block16 describes; in int8 every weight row (an output channel)
+ * is quantised with its own scale, as int8_quantize_rows describes.  Enqueued on
+ * `stream`; forwards enqueued later
  * on the same stream see the new weights, forwards enqueued earlier finish
  * with the old ones.  Returns MOE_ERR_WORKSPACE_TOO_SMALL if buf_bytes <
  * moe_weight_buffer_bytes. */
@@ -193,6 +195,51 @@ moe_status mxfp8_quantize_block32(const void* in, long long rows, int cols, long
 moe_status nvfp4_quantize_block16(const void* in, long long rows, int cols, long long ld_in,
                                   uint8_t* q, uint8_t* scales, float* row_scales,
                                   const int* live_rows_dev, void* stream);
+
+/* 8-bit integers with a scale for each row (no counterpart in the pages: an
+ * addition of this library, beside its MXFP8 and NVFP4).  Per row of bf16:
+ *   scales[r] = amax(row) / 127 in fp32 (1 for a row of zeros);
+ *   q[r, c]   = value / scales[r] in fp32, rounded to nearest even, in
+ *               [-127, 127].
+ * A row with a NaN or an infinity gets scale NaN and codes 0, so that every
+ * product with it is NaN.  in bf16 [rows, ld_in]; q int8 [rows, cols], scales
+ * fp32 [rows]; live_rows_dev as for mxfp8_quantize_block32.  cols a positive
+ * multiple of 8, ld_in >= cols and a multiple of 8, `in` 16-byte aligned, q
+ * 8-byte aligned. */
+moe_status int8_quantize_rows(const void* in, long long rows, int cols, long long ld_in, int8_t* q, float* scales,
+                              const int* live_rows_dev, void* stream);
+
+/* Matrix product in 8-bit integers with a scale for each token and channel:
+ *   out[t, c] = (float(sum_k x[t, k] * w[c, k]) * x_scales[t]) * w_scales[c]
+ * with the sum exact in int32, the conversion and the two products rounded to
+ * fp32 in this order, and, with out_bf16, the result rounded to bf16.
+ *   x  int8 [rows, ld_x], x_scales fp32 [rows]; w int8 [cols_out, cols_in] dense,
+ *   w_scales fp32 [cols_out] (any codes of [-128, 127]);
+ *   out fp32, or bf16 when out_bf16 is not 0, [rows, ld_out], any alignment of
+ *   its type; only rows < the live count and columns < cols_out are written.
+ *   live_rows_dev: nullable device int32, the live rows (clamped to [0, rows]).
+ *   status_dev: nullable device word that MOE_DEV_TIMEOUT is or-ed into should a
+ *   bounded on-device wait give up (the outputs are then not valid).
+ * cols_in: a multiple of 16 up to MOE_INT8_MAX_K; cols_out up to 2^20; rows up to
+ * 2^24; ld_x >= cols_in and a multiple of 16; x and w 16-byte aligned.  A row's
+ * results do not depend on the other rows or on the live count.  Enqueues work
+ * only. */
+#define MOE_INT8_MAX_K 131056
+moe_status int8_matmul(const int8_t* x, const float* x_scales, long long rows, int cols_in, long long ld_x,
+                       const int8_t* w, const float* w_scales, int cols_out, void* out, long long ld_out,
+                       int out_bf16, const int* live_rows_dev, unsigned* status_dev, void* stream);
+
+/* The same product of bf16 rows, quantised in the call as int8_quantize_rows
+ * does (the codes and scales stand in the workspace).  x bf16 [rows, ld_x], ld_x
+ * >= cols_in and a multiple of 8, 16-byte aligned; workspace:
+ * int8_linear_workspace_bytes(rows, cols_in), 256-byte aligned, nothing in it
+ * outlives the call; the other arguments as int8_matmul's, and the same bits as
+ * the two calls. */
+size_t int8_linear_workspace_bytes(long long rows, int cols_in);
+moe_status int8_linear(const void* x, long long rows, int cols_in, long long ld_x, const int8_t* w,
+                       const float* w_scales, int cols_out, void* out, long long ld_out, int out_bf16,
+                       const int* live_rows_dev, void* workspace, size_t ws_bytes, unsigned* status_dev,
+                       void* stream);
 
 /* Router ([P4] `_route`): for each live row t of logits (fp32 [capacity, E]),
  * softmax over the E experts, the k largest (ties: lower expert id), the k
@@ -277,8 +324,9 @@ moe_status moe_route_backward(const moe_plan* plan, const float* logits, const i
  *            p_j * y_j as fp32 FMAs from 0.0f, where
  *            y_j = W_down[e_j] . (silu(W_gate[e_j] . x_t) * (W_up[e_j] . x_t))
  *            with the SwiGLU row rounded to bf16 (or re-quantised to MXFP8,
- *            or to NVFP4 with the row's own scale) and y_j kept in fp32; in
- *            MXFP8 and NVFP4, x_t and the weights are quantised as their
+ *            or to NVFP4 with the row's own scale, or rounded to bf16 and then
+ *            quantised to int8 with the row's own scale) and y_j kept in fp32; in
+ *            MXFP8, NVFP4 and int8, x_t and the weights are quantised as their
  *            quantisation entry points describe.  Rows >= live count are not
  *            written.
  *            The plan's flags change this as MOE_FLAG_* states (bf16 out,
@@ -496,11 +544,11 @@ moe_status moe_ep_ipc_close(void* dev_ptr);
  *   perm    int32 [routes]: permuted row r holds route t*k + j
  *   inv     int32 [max_live, k]: padded intermediate row of route (t, j)
  *   pad_offsets int32 [E+1]: first padded intermediate row of each expert,
- *           a multiple of 32 (bf16) or 128 (MXFP8, NVFP4)
+ *           a multiple of 32 (bf16, int8) or 128 (MXFP8, NVFP4)
  *   h       intermediate rows [rows_padded, ceil(F/128)*128], bf16 or
- *           E4M3 codes, the columns past F zero
- *   xq      permuted x rows [rows_padded, ceil(H/128)*128], bf16 or E4M3
- *           codes, the columns past H zero; bf16 writes only the rows of
+ *           E4M3 or int8 codes, the columns past F zero
+ *   xq      permuted x rows [rows_padded, ceil(H/128)*128], bf16, E4M3
+ *           or int8 codes, the columns past H zero; bf16 writes only the rows of
  *           route tiles of more than 32 routes (the gate/up GEMM reads the
  *           x rows of smaller tiles in place)
  *   h_scales, xq_scales  MXFP8 and NVFP4 (else NULL).  MXFP8: E8M0 bytes
@@ -514,8 +562,8 @@ moe_status moe_ep_ipc_close(void* dev_ptr);
  *           byte of (row r, 16-element block b of the step) is at
  *           (r % 32) * 16 + (r / 32) * 4 + b.  NVFP4 h and xq are codes two
  *           per byte ([rows_padded, ceil(K/256)*128] bytes).
- *   xq_row_scales, h_row_scales  NVFP4 only: fp32 second-level scale per
- *           padded row;  h_fp32  the gate/up GEMM's fp32 h rows before
+ *   xq_row_scales, h_row_scales  NVFP4: fp32 second-level scale per padded row;
+ *           int8: the row's scale (else NULL);  h_fp32  the gate/up GEMM's fp32 h rows before
  *           quantisation: NVFP4 [rows_padded, ceil(F/256)*256]; MXFP8 plans
  *           made with MOE_FLAG_KEEP_H_FP32 [rows_padded, ceil(F/128)*128];
  *           else NULL. */
@@ -536,7 +584,9 @@ typedef struct {
     const float* h_row_scales;
     const float* h_fp32;
     const float* y;         /* fp32 [rows_padded, H]: the down GEMM's rows, row inv[t, j]
-                               the output of route (t, j) before the combine          */
+                               the output of route (t, j) before the combine       */
+    const void* h_bf16;     /* int8 only: the bf16 SwiGLU rows [rows_padded,
+                               ceil(F/128)*128] before they are quantised          */
 } moe_workspace_views;
 moe_status moe_get_workspace_views(const moe_plan* plan, const void* workspace,
                                    moe_workspace_views* views);

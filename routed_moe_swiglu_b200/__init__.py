@@ -27,7 +27,8 @@ __all__ = [
     "moe_weight_buffer_bytes", "moe_workspace_bytes", "alloc_weight_buffer", "alloc_workspace",
     "moe_prepare_weights", "mxfp8_quantize_block32", "nvfp4_quantize_block16", "moe_route_topk", "moe_forward",
     "moe_forward_with_events", "moe_balance_workspace_bytes", "moe_balance_loss", "moe_route_backward",
-    "moe_combine_backward", "MOE_MAX_SEQS",
+    "moe_combine_backward", "MOE_MAX_SEQS", "int8_quantize_rows", "int8_matmul", "int8_linear",
+    "int8_linear_workspace_bytes", "MOE_INT8_MAX_K",
     "moe_forward_noalloc", "MOE_NOALLOC_SCRATCH_BYTES", "moe_ep_dispatch", "moe_ep_combine",
     "MOE_NUM_STAGES", "STAGE_NAMES",
     "moe_get_workspace_views", "moe_get_device_status", "moe_clear_device_status",
@@ -46,7 +47,7 @@ MOE_FLAG_PROBS_IN_FC1 = 0x1
 MOE_FLAG_OUT_BF16 = 0x2
 MOE_FLAG_SQUARED_RELU = 0x4
 MOE_FLAG_KEEP_H_FP32 = 0x8
-_PRECISION = {"bf16": 0, "mxfp8": 1, "nvfp4": 2}
+_PRECISION = {"bf16": 0, "mxfp8": 1, "nvfp4": 2, "int8": 3}
 
 
 class MoeError(RuntimeError):
@@ -71,7 +72,8 @@ class _Views(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("route_ids", "route_probs", "offsets", "perm", "inv", "pad_offsets",
                                                  "h", "h_scales", "xq", "xq_scales")] + [
         ("rows_padded", ctypes.c_longlong), ("status", ctypes.c_void_p), ("xq_row_scales", ctypes.c_void_p),
-        ("h_row_scales", ctypes.c_void_p), ("h_fp32", ctypes.c_void_p), ("y", ctypes.c_void_p)]
+        ("h_row_scales", ctypes.c_void_p), ("h_fp32", ctypes.c_void_p), ("y", ctypes.c_void_p),
+        ("h_bf16", ctypes.c_void_p)]
 
 
 _lib = None
@@ -97,6 +99,10 @@ def load_library():
         "mxfp8_quantize_block32": ([P, LL, I, LL, P, P, P, P], I),
         "nvfp4_quantize_block16": ([P, LL, I, LL, P, P, P, P, P], I),
         "moe_route_topk": ([P, P, P, P, P, P], I),
+        "int8_quantize_rows": ([P, LL, I, LL, P, P, P, P], I),
+        "int8_matmul": ([P, P, LL, I, LL, P, P, I, P, LL, I, P, P, P], I),
+        "int8_linear_workspace_bytes": ([LL, I], SZ),
+        "int8_linear": ([P, LL, I, LL, P, P, I, P, LL, I, P, P, SZ, P, P], I),
         "moe_balance_workspace_bytes": ([P, I], SZ),
         "moe_balance_loss": ([P, P, P, P, P, I, F, F, P, P, P, P, P, P, P, SZ, P], I),
         "moe_route_backward": ([P, P, P, P, P, P, P, P, P, P, I, P, P, P], I),
@@ -266,6 +272,76 @@ def nvfp4_quantize_block16(x, q, scales, row_scales, live_rows=None, stream=None
     _check(load_library().nvfp4_quantize_block16(_ptr(x), rows, cols, x.stride(0), _ptr(q), _ptr(scales),
                                                  _ptr(row_scales), _ptr(live_rows), _stream(stream)),
            "nvfp4_quantize_block16")
+
+
+MOE_INT8_MAX_K = 131056
+
+
+def int8_quantize_rows(x, q, scales, live_rows=None, stream=None) -> None:
+    """x bf16 [rows, cols] (row stride in elements a multiple of 8) -> q int8 [rows, cols] with a scale
+    for each row, scales fp32 [rows] (include/moe.h)."""
+    _rows_of("x", x, "bfloat16")
+    rows, cols = x.shape
+    _dense("q", q, "int8", (rows, cols))
+    _dense("scales", scales, "float32", (rows,))
+    _check(load_library().int8_quantize_rows(_ptr(x), rows, cols, _ld(x), _ptr(q), _ptr(scales), _ptr(live_rows),
+                                             _stream(stream)), "int8_quantize_rows")
+
+
+def _rows_of(name: str, t, dtype: str) -> None:
+    """`t` must be a matrix of the dtype named whose rows are dense (any row stride)."""
+    import torch
+
+    if t.dtype is not getattr(torch, dtype):
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with dense rows")
+
+
+def _ld(t) -> int:
+    """Row stride; a single row's may be anything, and is then its length."""
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _int8_out(x, wq, w_scales, out) -> int:
+    import torch
+
+    N, K = wq.shape
+    _dense("wq", wq, "int8", (N, x.shape[1]))
+    _dense("w_scales", w_scales, "float32", (N,))
+    bf16 = out.dtype is torch.bfloat16
+    _rows_of("out", out, "bfloat16" if bf16 else "float32")
+    if tuple(out.shape) != (x.shape[0], N):
+        raise ValueError(f"out must have shape {(x.shape[0], N)}, not {tuple(out.shape)}")
+    return int(bf16)
+
+
+def int8_matmul(xq, x_scales, wq, w_scales, out, live_rows=None, status=None, stream=None) -> None:
+    """out[t, c] = sum_k xq[t, k] * wq[c, k] * x_scales[t] * w_scales[c]: xq int8 [rows, K] (row stride a
+    multiple of 16), wq int8 [N, K], out fp32 or bf16 [rows, N] (include/moe.h)."""
+    _rows_of("xq", xq, "int8")
+    bf16 = _int8_out(xq, wq, w_scales, out)
+    rows, K = xq.shape
+    _dense("x_scales", x_scales, "float32", (rows,))
+    _check(load_library().int8_matmul(_ptr(xq), _ptr(x_scales), rows, K, _ld(xq), _ptr(wq), _ptr(w_scales),
+                                      wq.shape[0], _ptr(out), _ld(out), bf16, _ptr(live_rows), _ptr(status),
+                                      _stream(stream)), "int8_matmul")
+
+
+def int8_linear_workspace_bytes(rows: int, cols_in: int) -> int:
+    return int(load_library().int8_linear_workspace_bytes(int(rows), int(cols_in)))
+
+
+def int8_linear(x, wq, w_scales, out, workspace, live_rows=None, status=None, stream=None) -> None:
+    """int8_matmul of bf16 rows x [rows, K] (row stride a multiple of 8), quantised in the call;
+    workspace: int8_linear_workspace_bytes(rows, K) bytes."""
+    _rows_of("x", x, "bfloat16")
+    bf16 = _int8_out(x, wq, w_scales, out)
+    rows, K = x.shape
+    _check(load_library().int8_linear(_ptr(x), rows, K, _ld(x), _ptr(wq), _ptr(w_scales), wq.shape[0], _ptr(out),
+                                      _ld(out), bf16, _ptr(live_rows), _ptr(workspace),
+                                      workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)),
+           "int8_linear")
 
 
 def moe_route_topk(plan: Plan, logits, live_count, ids, probs, stream=None) -> None:

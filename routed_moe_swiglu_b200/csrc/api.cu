@@ -7,6 +7,7 @@
 #include <new>
 
 #include "ep.cuh"
+#include "int8.cuh"
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -71,6 +72,7 @@ static void compute_layouts(moe_plan* p) {
     const size_t L = (size_t)p->max_live;
     const size_t R = (size_t)p->rows_pad;
     const bool fp8 = p->d.precision == MOE_MXFP8;
+    const bool i8 = p->d.precision == MOE_INT8;
     WsLayout& w = p->ws;
     size_t off = 0;
     auto take = [&off](size_t bytes) {
@@ -89,7 +91,7 @@ static void compute_layouts(moe_plan* p) {
     w.inv = take(L * k * 4);
     const size_t mtiles = (size_t)p->max_m_tiles;
     const bool fp4 = p->d.precision == MOE_NVFP4;
-    w.ready = fp8 || fp4 ? 0 : take(mtiles * 4);
+    w.ready = fp8 || fp4 || i8 ? 0 : take(mtiles * 4);
     w.xg = w.hf = w.hg = 0;
     if (fp4) {
         // codes two per byte; four 512-byte scale blocks per 128-row tile and K block of 256
@@ -99,6 +101,13 @@ static void compute_layouts(moe_plan* p) {
         w.hf = take(R * (size_t)p->fp * 4);
         w.h = take(R * (size_t)p->fp / 2);
         w.hs = take(mtiles * p->ks2 * 4 * kSfBlock);
+        w.hg = take(R * 4);
+    } else if (i8) {
+        w.xq = take(R * (size_t)p->hp);
+        w.xs = w.hs = 0;
+        w.xg = take(R * 4);
+        w.hf = take(R * (size_t)p->fp * 2);  // bf16 h rows, before the pass that quantises them
+        w.h = take(R * (size_t)p->fp);
         w.hg = take(R * 4);
     } else if (fp8) {
         w.xq = take(R * (size_t)p->hp);
@@ -124,6 +133,11 @@ static void compute_layouts(moe_plan* p) {
         b.w2 = take(E * H * (size_t)p->fp / 2);
         b.w2s = take(E * p->nt2 * p->ks2 * 4 * kSfBlock);
         b.wg = take(E * 2 * 4);
+    } else if (i8) {
+        b.w1 = take(E * (size_t)p->w1r * (size_t)p->hp);
+        b.w1s = take(E * (size_t)p->w1r * 4);
+        b.w2 = take(E * (size_t)p->hr * (size_t)p->fp);
+        b.w2s = take(E * (size_t)p->hr * 4);
     } else if (fp8) {
         b.w1 = take(E * (size_t)p->w1r * (size_t)p->hp);
         b.w1s = take(E * p->nt1 * p->ks1 * kSfBlock);
@@ -165,8 +179,10 @@ moe_status moe_plan_create(const moe_desc* desc, moe_plan** plan_out) {
     if (desc == nullptr || plan_out == nullptr) return MOE_ERR_INVALID_ARG;
     *plan_out = nullptr;
     const moe_desc& d = *desc;
-    if (d.precision != MOE_BF16 && d.precision != MOE_MXFP8 && d.precision != MOE_NVFP4) return MOE_ERR_INVALID_ARG;
-    const bool blockscaled = d.precision != MOE_BF16;  // MXFP8 or NVFP4: one CTA, 128-row tiles
+    if (d.precision != MOE_BF16 && d.precision != MOE_MXFP8 && d.precision != MOE_NVFP4 && d.precision != MOE_INT8)
+        return MOE_ERR_INVALID_ARG;
+    // MXFP8 or NVFP4: one CTA, 128-row tiles; bf16 and int8: CTA pairs, 256-route tiles
+    const bool blockscaled = d.precision == MOE_MXFP8 || d.precision == MOE_NVFP4;
     if (d.hidden <= 0 || d.ffn <= 0 || d.num_experts <= 0 || d.top_k <= 0 || d.capacity <= 0)
         return MOE_ERR_UNSUPPORTED;
     const int mult = blockscaled ? 32 : 8;
@@ -177,7 +193,7 @@ moe_status moe_plan_create(const moe_desc* desc, moe_plan** plan_out) {
     if (d.max_live_rows < 0 || d.max_live_rows > d.capacity) return MOE_ERR_UNSUPPORTED;
     if ((d.flags & ~(MOE_FLAG_PROBS_IN_FC1 | MOE_FLAG_OUT_BF16 | MOE_FLAG_SQUARED_RELU | MOE_FLAG_KEEP_H_FP32)) != 0)
         return MOE_ERR_INVALID_ARG;
-    if ((d.flags & MOE_FLAG_KEEP_H_FP32) != 0 && d.precision == MOE_BF16) return MOE_ERR_INVALID_ARG;
+    if ((d.flags & MOE_FLAG_KEEP_H_FP32) != 0 && !blockscaled) return MOE_ERR_INVALID_ARG;
     if (!(d.gate_up_clamp >= 0.0f) || d.gate_up_clamp > 3.0e38f) return MOE_ERR_INVALID_ARG;
     moe_plan* p = new (std::nothrow) moe_plan();
     if (p == nullptr) return MOE_ERR_INVALID_ARG;
@@ -244,6 +260,7 @@ moe_status moe_prepare_weights(const moe_plan* plan, const void* w_gate, const v
     const auto* dn = static_cast<const __nv_bfloat16*>(w_down);
     const cudaError_t e = plan->d.precision == MOE_MXFP8   ? launch_prepare_mxfp8(plan, g, u, dn, kernel_buf, s)
                           : plan->d.precision == MOE_NVFP4 ? launch_prepare_nvfp4(plan, g, u, dn, kernel_buf, s)
+                          : plan->d.precision == MOE_INT8  ? launch_prepare_int8(plan, g, u, dn, kernel_buf, s)
                                                            : launch_prepare_bf16(plan, g, u, dn, kernel_buf, s);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -322,9 +339,10 @@ static moe_status forward_impl(const moe_plan* plan, const void* x, const float*
     // TMA descriptors for this call's buffers (host-side encoding only)
     const bool fp8 = plan->d.precision == MOE_MXFP8;
     const bool fp4 = plan->d.precision == MOE_NVFP4;
+    const bool i8 = plan->d.precision == MOE_INT8;
     const unsigned long long R = (unsigned long long)plan->rows_pad;
     const unsigned long long uH = (unsigned long long)H, uE = (unsigned long long)E;
-    const CUtensorMapDataType dt = fp8 || fp4 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapDataType dt = fp8 || fp4 || i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
     CUtensorMap tA1, tA2;  // weight operands
     BoxMaps8 rB1, rB2;     // route-row operands (x rows, h rows)
     CUtensorMap tX;        // bf16: x rows, gathered by token
@@ -350,6 +368,29 @@ static moe_status forward_impl(const moe_plan* plan, const void* x, const float*
             const unsigned box[3] = {128, 32u * (unsigned)(i + 1), 2};
             if (!make_tensor_map(&rB1.m[i], dt, 3, ws + L.xq, dX, sW1, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
                 !make_tensor_map(&rB2.m[i], dt, 3, ws + L.h, dH, sW2, box, CU_TENSOR_MAP_SWIZZLE_128B))
+                return MOE_ERR_CUDA;
+        }
+    } else if (i8) {
+        // int8 (CTA pairs): K stage = 256 elements = two 128-byte swizzle atoms.  Weights are
+        // blocks of [128 rows][128 codes], the blocks of a row block after one another along K;
+        // route rows are addressed as (b % 128, row, b / 128), so that both operands land as
+        // [atom][row][128 codes], one route-row map per N/2 in {16, ..., 128}.
+        const unsigned long long hp = (unsigned long long)plan->hp, fpp = (unsigned long long)plan->fp;
+        const unsigned box128[3] = {128, 128, 2};
+        const unsigned long long dW1[3] = {128ull, 128ull, uE * (unsigned long long)plan->w1r / 128 * (hp / 128)};
+        const unsigned long long dW2[3] = {128ull, 128ull, uE * (unsigned long long)plan->hr / 128 * (fpp / 128)};
+        const unsigned long long sWb[2] = {128ull, 128ull * 128ull};
+        const unsigned long long sX[2] = {hp, 128ull};
+        const unsigned long long sH[2] = {fpp, 128ull};
+        const unsigned long long dX[3] = {128ull, R, hp / 128};
+        const unsigned long long dH[3] = {128ull, R, fpp / 128};
+        if (!make_tensor_map(&tA1, dt, 3, wb + plan->wb.w1, dW1, sWb, box128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+            !make_tensor_map(&tA2, dt, 3, wb + plan->wb.w2, dW2, sWb, box128, CU_TENSOR_MAP_SWIZZLE_128B))
+            return MOE_ERR_CUDA;
+        for (int i = 0; i < 8; ++i) {
+            const unsigned box[3] = {128, 16u * (unsigned)(i + 1), 2};
+            if (!make_tensor_map(&rB1.m[i], dt, 3, ws + L.xq, dX, sX, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+                !make_tensor_map(&rB2.m[i], dt, 3, ws + L.h, dH, sH, box, CU_TENSOR_MAP_SWIZZLE_128B))
                 return MOE_ERR_CUDA;
         }
     } else {
@@ -402,7 +443,7 @@ static moe_status forward_impl(const moe_plan* plan, const void* x, const float*
     int* perm = reinterpret_cast<int*>(ws + L.perm);
     int* inv = reinterpret_cast<int*>(ws + L.inv);
     int4* tiles = reinterpret_cast<int4*>(ws + L.tiles);
-    int* ready = fp8 || fp4 ? nullptr : reinterpret_cast<int*>(ws + L.ready);  // bf16 only
+    int* ready = fp8 || fp4 || i8 ? nullptr : reinterpret_cast<int*>(ws + L.ready);  // bf16 only
     e = launch_permute(plan, live_count_dev, r_ids, reinterpret_cast<int*>(ws + L.blkcnt),
                        reinterpret_cast<int*>(ws + L.offsets), reinterpret_cast<int*>(ws + L.padoff), tiles, perm, inv,
                        ready, status, s);
@@ -417,9 +458,49 @@ static moe_status forward_impl(const moe_plan* plan, const void* x, const float*
         e = launch_gather_nvfp4(static_cast<const __nv_bfloat16*>(x), live_count_dev, max_live, H, (int)plan->hp, k,
                                 inv, ws + L.xq, ws + L.xs, reinterpret_cast<float*>(ws + L.xg), status, s);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
+    } else if (i8) {
+        e = launch_gather_int8(static_cast<const __nv_bfloat16*>(x), live_count_dev, max_live, H, (int)plan->hp, k, inv,
+                               ws + L.xq, reinterpret_cast<float*>(ws + L.xg), status, s);
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
     }
 
     const long long m_tiles = plan->max_m_tiles;
+    const bool probs_in_fc1 = (plan->d.flags & MOE_FLAG_PROBS_IN_FC1) != 0;
+    if (i8) {
+        Int8Gemm g{};
+        g.tiles = tiles;
+        g.status_words = status;
+        g.status_flags = status + kStFlags;
+        g.wait_limit_ns = kWaitLimitNs;
+        g.perm = perm;
+        g.out = ws + L.hf;
+        g.out_ld = g.out_cols = (int)plan->fp;
+        g.n_tiles = plan->nt1;
+        g.atoms = plan->ks1;
+        g.a_rows = plan->w1r;
+        g.row_scale = reinterpret_cast<const float*>(ws + L.xg);
+        g.w_scale = reinterpret_cast<const float*>(wb + plan->wb.w1s);
+        g.route_probs = probs_in_fc1 ? r_probs : nullptr;
+        g.clamp = plan->d.gate_up_clamp;
+        g.relu2 = (plan->d.flags & MOE_FLAG_SQUARED_RELU) != 0;
+        if (!mark(3)) return MOE_ERR_CUDA;
+        e = launch_gemm1_int8(tA1, rB1, g, m_tiles * g.n_tiles, s);
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
+        // h rows -> int8 with a scale per row (timed with the gate/up stage)
+        e = launch_quantize_h_int8(reinterpret_cast<const __nv_bfloat16*>(ws + L.hf), live_count_dev, max_live, k,
+                                   (int)plan->fp, inv, ws + L.h, reinterpret_cast<float*>(ws + L.hg), status, s);
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
+        g.out = ws + L.y;
+        g.out_ld = g.out_cols = H;
+        g.n_tiles = plan->nt2;
+        g.atoms = plan->ks2;
+        g.a_rows = plan->hr;
+        g.row_scale = reinterpret_cast<const float*>(ws + L.hg);
+        g.w_scale = reinterpret_cast<const float*>(wb + plan->wb.w2s);
+        if (!mark(4)) return MOE_ERR_CUDA;
+        e = launch_gemm2_int8(tA2, rB2, g, m_tiles * g.n_tiles, s);
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
+    } else {
     GemmParams g1{};
     g1.tiles = tiles;
     g1.status_words = status;
@@ -438,7 +519,6 @@ static moe_status forward_impl(const moe_plan* plan, const void* x, const float*
     g1.sf_ks_out = plan->ks2;
     g1.perm = perm;
     g1.top_k = k;
-    const bool probs_in_fc1 = (plan->d.flags & MOE_FLAG_PROBS_IN_FC1) != 0;
     g1.route_probs = probs_in_fc1 ? r_probs : nullptr;
     g1.clamp = plan->d.gate_up_clamp;
     g1.relu2 = (plan->d.flags & MOE_FLAG_SQUARED_RELU) != 0;
@@ -482,6 +562,7 @@ static moe_status forward_impl(const moe_plan* plan, const void* x, const float*
         : fp4 ? launch_gemm2_nvfp4(tA2, rB2, g2, m_tiles * g2.n_tiles, s)
               : launch_gemm2_bf16_pair(tA2, rB2, g2, m_tiles * g2.n_tiles, s);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
+    }
     if (!mark(5)) return MOE_ERR_CUDA;
 
     // the probabilities were applied in the gate/up epilogue: the combine adds the rows
@@ -536,7 +617,7 @@ moe_status moe_ep_dispatch(const moe_plan* plan, int ep_size, const void* x, con
     unsigned* status = reinterpret_cast<unsigned*>(ws + L.status);
     int* r_ids = reinterpret_cast<int*>(ws + L.r_ids);
     float* r_probs = reinterpret_cast<float*>(ws + L.r_probs);
-    const bool blockscaled = plan->d.precision != MOE_BF16;
+    const bool counts_copies = plan->d.precision == MOE_BF16;
     cudaError_t e = have_logits ? launch_route_topk(logits, live_count_dev, max_live, E, k, r_ids, r_probs, status, s)
                                 : launch_canon_routes(ids, probs, live_count_dev, max_live, E, k, r_ids, r_probs,
                                                       status, s);
@@ -546,7 +627,7 @@ moe_status moe_ep_dispatch(const moe_plan* plan, int ep_size, const void* x, con
     int* padoff = reinterpret_cast<int*>(ws + L.padoff);
     e = launch_permute(plan, live_count_dev, r_ids, reinterpret_cast<int*>(ws + L.blkcnt), offsets, padoff,
                        reinterpret_cast<int4*>(ws + L.tiles), reinterpret_cast<int*>(ws + L.perm), inv,
-                       blockscaled ? nullptr : reinterpret_cast<int*>(ws + L.ready), status, s);
+                       counts_copies ? reinterpret_cast<int*>(ws + L.ready) : nullptr, status, s);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     e = launch_ep_pack(x, live_count_dev, max_live, H, k, r_ids, r_probs, inv, offsets, padoff, E, ep_size,
                        (plan->d.flags & MOE_FLAG_PROBS_IN_FC1) != 0, send_x, send_ids, send_probs, send_counts,
@@ -613,7 +694,7 @@ moe_status moe_ep_peer_dispatch(const moe_plan* plan, int ep_size, int rank, con
     unsigned* status = reinterpret_cast<unsigned*>(ws + L.status);
     int* r_ids = reinterpret_cast<int*>(ws + L.r_ids);
     float* r_probs = reinterpret_cast<float*>(ws + L.r_probs);
-    const bool blockscaled = plan->d.precision != MOE_BF16;
+    const bool counts_copies = plan->d.precision == MOE_BF16;
     cudaError_t e = have_logits ? launch_route_topk(logits, live_count_dev, max_live, E, k, r_ids, r_probs, status, s)
                                 : launch_canon_routes(ids, probs, live_count_dev, max_live, E, k, r_ids, r_probs,
                                                       status, s);
@@ -623,7 +704,7 @@ moe_status moe_ep_peer_dispatch(const moe_plan* plan, int ep_size, int rank, con
     int* padoff = reinterpret_cast<int*>(ws + L.padoff);
     e = launch_permute(plan, live_count_dev, r_ids, reinterpret_cast<int*>(ws + L.blkcnt), offsets, padoff,
                        reinterpret_cast<int4*>(ws + L.tiles), reinterpret_cast<int*>(ws + L.perm), inv,
-                       blockscaled ? nullptr : reinterpret_cast<int*>(ws + L.ready), status, s);
+                       counts_copies ? reinterpret_cast<int*>(ws + L.ready) : nullptr, status, s);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     const EpRegionLayout lay = ep_region_layout(H, max_live, k, ep_size);
     e = launch_ep_peer_pack(x, live_count_dev, max_live, H, k, r_ids, r_probs, inv, offsets, padoff, E, ep_size, rank,
@@ -706,14 +787,16 @@ moe_status moe_get_workspace_views(const moe_plan* plan, const void* workspace, 
     v->inv = reinterpret_cast<const int*>(ws + L.inv);
     v->pad_offsets = reinterpret_cast<const int*>(ws + L.padoff);
     v->h = ws + L.h;
-    const bool scaled = plan->d.precision != MOE_BF16;
-    const bool fp4 = plan->d.precision == MOE_NVFP4;
+    const bool i8 = plan->d.precision == MOE_INT8;
+    const bool scaled = plan->d.precision != MOE_BF16 && !i8;
+    const bool fp4 = plan->d.precision == MOE_NVFP4 || i8;  // a scale per row
     v->h_scales = scaled ? ws + L.hs : nullptr;
     v->xq = ws + L.xq;
     v->xq_scales = scaled ? ws + L.xs : nullptr;
     v->xq_row_scales = fp4 ? reinterpret_cast<const float*>(ws + L.xg) : nullptr;
     v->h_row_scales = fp4 ? reinterpret_cast<const float*>(ws + L.hg) : nullptr;
-    v->h_fp32 = L.hf != 0 ? reinterpret_cast<const float*>(ws + L.hf) : nullptr;
+    v->h_bf16 = i8 ? ws + L.hf : nullptr;
+    v->h_fp32 = L.hf != 0 && !i8 ? reinterpret_cast<const float*>(ws + L.hf) : nullptr;
     v->y = reinterpret_cast<const float*>(ws + L.y);
     v->rows_padded = plan->rows_pad;
     v->status = reinterpret_cast<const unsigned*>(ws + L.status);

@@ -1,0 +1,556 @@
+// gemm_int8.cu -- matrix products in 8-bit integers with an fp32 scale for each
+// activation row and each weight row: the two grouped expert products and the
+// dense product, each tile computed by a pair of CTAs on two SMs with one
+// tcgen05 MMA (cta_group::2, kind::i8: int8 operands, exact int32 sums).
+//
+//   out[t, c] = (float(sum_k x[t, k] * w[c, k]) * x_scale[t]) * w_scale[c]
+//
+// The sum is exact, so it does not depend on the tile, on the K order or on how
+// K is split; the conversion and the two products round once each.
+//
+// Weights are the MMA's M operand (256 rows, 128 per CTA) and activation rows
+// its N operand (a multiple of 32 up to 256), so that an expert's last tile and
+// a short batch cost their own row count, as in the bf16 kernels:
+//   gate/up  256 rows of W1 (gate and up interleaved in groups of 16, so that
+//            the warp reading a TMEM quarter holds both of 16 f) -> SwiGLU ->
+//            bf16 h rows, quantised by a pass of their own (a row's scale needs
+//            all of F)
+//   down     256 rows of W2 -> fp32 y rows
+//   dense    256 weight rows -> bf16 or fp32 rows of out
+// A K stage is two 128-byte swizzle atoms, 256 elements, 8 MMAs.  Where K has an
+// odd number of atoms the last stage's second one holds zeros on the activation
+// side; what stands there on the weight side is then of no account (integers
+// have no NaN).
+//
+// Roles (10 warps per CTA): warp 0 issues TMA loads; warp 1 owns TMEM and, in
+// CTA 0, issues the MMAs; warps 2-9 drain two accumulators of 256 columns.
+// Every mbarrier wait is bounded; the pair meets in cluster barriers only at
+// start-up and before TMEM is released.
+#include "int8.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kStagesMax = 5;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (2 + kEpiWarps) * 32;
+constexpr int kPairM = 256;
+constexpr int kAtoms = 2;                            // 128-byte swizzle atoms per stage
+constexpr uint32_t kAtomBytes = 128 * 128;           // 128 rows of 128 bytes
+constexpr uint32_t kABytes = kAtoms * kAtomBytes;    // 32 KB: this CTA's 128 weight rows
+constexpr uint32_t kBBytesMax = kAtoms * kAtomBytes; // up to 128 activation rows per CTA
+constexpr uint32_t kAccCols = 256;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kStageRegion = 4 * (kABytes + 16384);  // also 3 * (32 + 32) and 5 * (32 + 6) KB
+constexpr uint32_t kEpiBox = 32 * 32 * 4 + 128;           // transpose box and 32 row scales of a warp
+constexpr size_t kSmemBytes = 1024 + kStageRegion + kEpiWarps * kEpiBox + 256;
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+static_assert(kStageRegion >= 3 * (kABytes + kBBytesMax), "three full-width stages");
+
+struct __align__(8) Barriers {
+    uint64_t full[kStagesMax];   // CTA 0's counts both CTAs' loads of a stage
+    uint64_t empty[kStagesMax];  // each CTA's: its stage may be refilled
+    uint64_t acc_full[2];        // each CTA's: its accumulator rows are ready
+    uint64_t acc_empty[2];       // CTA 0's: both CTAs drained the accumulator
+    uint64_t done;
+    uint32_t tmem_base;
+    int abort_flag;
+};
+
+// Instruction descriptor of kind::i8: int32 sums of signed 8-bit A and B, both K-major.
+__host__ __device__ constexpr uint32_t idesc_i8(int M, int N) {
+    return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* map, uint32_t mbar_cluster, int c0,
+                                                 int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, "
+        "%4}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(mbar_cluster), "r"(c0), "r"(c1)
+        : "memory");
+}
+
+__device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+// x clamped to [-c, c]; a NaN (a row that holds one) stays NaN.
+__device__ __forceinline__ float clamp_nan(float x, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;\n\tmin.NaN.f32 %0, %0, %3;" : "=f"(r) : "f"(x), "f"(-c), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float swiglu_value(float g, float u, float clamp) {
+    if (clamp > 0.0f) {
+        g = clamp_nan(g, clamp);
+        u = clamp_nan(u, clamp);
+    }
+    return silu_f(g) * u;
+}
+
+__device__ __forceinline__ int tile_n(int nvalid) { return (nvalid + 31) & ~31; }
+
+struct StageCfg {
+    int n;       // stages
+    uint32_t b;  // activation slot bytes
+};
+__device__ __forceinline__ StageCfg stage_cfg(int widest_tile) {
+    const int hb = tile_n(widest_tile) >> 1;  // activation rows per CTA
+    if (hb <= 16) return {5, 4096u};
+    if (hb <= 64) return {4, 16384u};
+    return {3, kBBytesMax};
+}
+
+enum { kGateUp = 0, kDown = 1, kDense = 2 };
+
+// Tile t of the launch: {expert, first activation row, valid rows, first permuted row}.
+template <int kMode>
+__device__ __forceinline__ int4 tile_of(const Int8Gemm& p, int mt, int rows) {
+    if (kMode != kDense) return __ldg(p.tiles + mt);
+    const int m0 = mt * kRouteTile;
+    return make_int4(0, m0, min(kRouteTile, rows - m0), m0);
+}
+
+// Four outputs of one row, from int32 sums.
+__device__ __forceinline__ float4 scaled4(int4 v, float xs, float4 ws) {
+    return make_float4(__int2float_rn(v.x) * xs * ws.x, __int2float_rn(v.y) * xs * ws.y,
+                       __int2float_rn(v.z) * xs * ws.z, __int2float_rn(v.w) * xs * ws.w);
+}
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+template <int kMode>
+__device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const BoxMaps8* tmB, const Int8Gemm& p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sEpi = smem + kStageRegion;
+    Barriers* bars = reinterpret_cast<Barriers*>(sEpi + kEpiWarps * kEpiBox);
+    volatile int* abort_flag = &bars->abort_flag;
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    const int pair = (int)cluster_id_x();
+    const int npairs = (int)cluster_count_x();
+    pdl_trigger();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStagesMax; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&bars->acc_full[b], 1);
+            mbar_init(&bars->acc_empty[b], 2 * kEpiWarps);
+        }
+        mbar_init(&bars->done, 1);
+        bars->abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(&bars->tmem_base, kTmemCols);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();  // both CTAs' barriers and TMEM exist before any cross-CTA traffic
+    tc_fence_after_sync();
+    const uint32_t tmem_base = bars->tmem_base;
+    pdl_wait();
+
+    int num_m, rows = 0, widest;
+    if (kMode == kDense) {
+        rows = p.live != nullptr ? clamp_live(p.live, p.rows) : p.rows;
+        num_m = (rows + kRouteTile - 1) / kRouteTile;
+        widest = min(rows, kRouteTile);
+    } else {
+        num_m = forward_poisoned(p.status_words) ? 0 : (int)p.status_words[kStNumMTiles];
+        widest = (int)p.status_words[kStMaxTileRows];
+    }
+    const int total_tiles = num_m * p.n_tiles;
+    const int kb_count = (p.atoms + kAtoms - 1) / kAtoms;
+    const StageCfg sc = stage_cfg(widest);
+    const int kStages = sc.n;
+    const uint32_t kBBytes = sc.b;
+    uint8_t* sB = smem + kStages * kABytes;
+    auto timed_out = [&]() {
+        *abort_flag = 1;
+        if (p.status_flags != nullptr) atomicOr(p.status_flags, MOE_DEV_TIMEOUT);
+    };
+
+    if (warp == 0) {
+        if (lane == 0) {
+            // ---------------- TMA producer (one thread of each CTA)
+            tma_prefetch_desc(&tmA);
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            int last_phase[kStagesMax];
+            for (int s = 0; s < kStagesMax; ++s) last_phase[s] = -1;
+            for (int t = pair; t < total_tiles && ok; t += npairs) {
+                const int mt = t / p.n_tiles, nt = t - mt * p.n_tiles;
+                const int4 ti = tile_of<kMode>(p, mt, rows);
+                const int hb = tile_n(ti.z) >> 1;
+                const uint32_t tx = 2u * (kABytes + (uint32_t)hb * (kAtoms * 128u));
+                const CUtensorMap* mb = &tmB->m[(hb >> 4) - 1];
+                const int w_row = nt * kPairM + 128 * (int)rank;
+                const int a_atom0 = kMode == kDense
+                                        ? 0
+                                        : (int)(((long long)ti.x * p.a_rows + w_row) / 128 * p.atoms);
+                const int b_row = ti.y + hb * (int)rank;
+                for (int kb = 0; kb < kb_count; ++kb) {
+                    if (!mbar_wait_bounded(&bars->empty[stage], phase ^ 1u, abort_flag, p.wait_limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t full0 = map_to_cta(smem_u32(&bars->full[stage]), 0);
+                    if (leader) {
+                        mbar_arrive_expect_tx(&bars->full[stage], tx);
+                        last_phase[stage] = (int)phase;
+                    }
+                    uint8_t* a_dst = sA + stage * kABytes;
+                    uint8_t* b_dst = sB + stage * kBBytes;
+                    if (kMode == kDense) {
+                        // atoms of plain rows; columns from K on are filled with zeros
+#pragma unroll
+                        for (int at = 0; at < kAtoms; ++at) {
+                            const int k0 = (kb * kAtoms + at) * 128;
+                            tma_load_2d_pair(a_dst + at * kAtomBytes, &tmA, full0, k0, w_row);
+                            tma_load_2d_pair(b_dst + (uint32_t)at * (uint32_t)hb * 128u, mb, full0, k0, b_row);
+                        }
+                    } else {
+                        tma_load_3d_pair(a_dst, &tmA, full0, 0, 0, a_atom0 + kb * kAtoms);
+                        tma_load_3d_pair(b_dst, mb, full0, 0, b_row, kb * kAtoms);
+                    }
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok) {
+                timed_out();
+                if (leader) {  // copies already issued land before shared memory goes away
+                    for (int s = 0; s < kStages; ++s)
+                        if (last_phase[s] >= 0) {
+                            volatile int never = 0;
+                            (void)mbar_wait_bounded(&bars->full[s], (uint32_t)last_phase[s], &never, 100000000ull);
+                        }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            // ---------------- pair MMA issuer (CTA 0)
+            int stage = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            int it = 0;
+            for (int t = pair; t < total_tiles && ok; t += npairs, ++it) {
+                const int buf = it & 1;
+                const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
+                const int n = tile_n(tile_of<kMode>(p, t / p.n_tiles, rows).z);
+                const uint32_t idesc = idesc_i8(kPairM, n);
+                const uint32_t b_atom = (uint32_t)(n >> 1) * 128u;  // bytes of one atom of this CTA's rows
+                if (!mbar_wait_bounded(&bars->acc_empty[buf], acc_phase ^ 1u, abort_flag, p.wait_limit_ns)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint32_t d_tmem = tmem_base + (uint32_t)buf * kAccCols;
+                for (int kb = 0; kb < kb_count; ++kb) {
+                    if (!mbar_wait_bounded(&bars->full[stage], phase, abort_flag, p.wait_limit_ns)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    const uint32_t a_addr = smem_u32(sA + stage * kABytes);
+                    const uint32_t b_addr = smem_u32(sB + stage * kBBytes);
+#pragma unroll
+                    for (int kk = 0; kk < kAtoms * 4; ++kk) {  // 32 elements of K each
+                        const uint32_t koff = (uint32_t)(kk & 3) * 32;
+                        mma_i8_pair(d_tmem, sdesc_kmajor_sw128(a_addr + (uint32_t)(kk >> 2) * kAtomBytes + koff),
+                                    sdesc_kmajor_sw128(b_addr + (uint32_t)(kk >> 2) * b_atom + koff), idesc,
+                                    (kb | kk) != 0 ? 1u : 0u);
+                    }
+                    mma_commit_pair_multicast(&bars->empty[stage], 0x3);  // both CTAs may refill the stage
+                    if (++stage == kStages) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                mma_commit_pair_multicast(&bars->acc_full[buf], 0x3);
+            }
+            if (!ok) timed_out();
+            mma_commit_pair(&bars->done);
+            volatile int never = 0;
+            (void)mbar_wait_bounded(&bars->done, 0, &never, 100000000ull);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- epilogue: warps 2..9
+        const int ew = warp - 2;
+        const int quad = warp & 3;  // TMEM lane quarter this warp may read
+        const int half = ew >> 2;   // this warp takes the 32-row chunks c with c % 2 == half
+        const uint32_t acc_empty0[2] = {map_to_cta(smem_u32(&bars->acc_empty[0]), 0),
+                                        map_to_cta(smem_u32(&bars->acc_empty[1]), 0)};
+        uint8_t* tbuf = sEpi + (size_t)ew * kEpiBox;
+        float* s_xs = reinterpret_cast<float*>(tbuf + 32 * 32 * 4);
+        int it = 0;
+        for (int t = pair; t < total_tiles; t += npairs, ++it) {
+            const int buf = it & 1;
+            const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
+            const int mt = t / p.n_tiles, nt = t - mt * p.n_tiles;
+            const int4 ti = tile_of<kMode>(p, mt, rows);
+            const int nch = tile_n(ti.z) >> 5;
+            const int w0 = nt * kPairM + 128 * (int)rank + 32 * quad;  // this warp's first weight row
+            const bool got = __all_sync(0xffffffffu,
+                                        mbar_wait_bounded(&bars->acc_full[buf], acc_phase, abort_flag, p.wait_limit_ns));
+            if (!got) {
+                if (lane == 0) timed_out();
+                break;
+            }
+            tc_fence_after_sync();
+            const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)buf * kAccCols;
+            if (kMode == kGateUp) {
+                // lanes are weight rows: their scale in a register, the 32 activation rows' in shared memory
+                const float ws = __ldg(p.w_scale + (size_t)ti.x * p.a_rows + w0 + lane);
+                __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(p.out);
+                const bool lo = lane < 16;
+                const int f0 = p.relu2 ? w0 : w0 >> 1;  // first of this warp's 32 (16) f
+                if (f0 < p.out_cols) {
+#pragma unroll 1
+                    for (int c = half; c < nch; c += 2) {
+                        uint32_t v[32];
+                        tmem_ld_32x32b_x32(taddr + c * 32, v);
+                        const bool row_ok = c * 32 + lane < ti.z;
+                        s_xs[lane] = row_ok ? __ldg(p.row_scale + ti.y + c * 32 + lane) : 0.0f;
+                        float pv = 1.0f;
+                        if (p.route_probs != nullptr && row_ok)
+                            pv = __ldg(p.route_probs + __ldg(p.perm + ti.w + c * 32 + lane));
+                        tmem_ld_wait();
+                        __syncwarp();
+                        float g[32];
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) g[j] = __int2float_rn((int)v[j]) * s_xs[j] * ws;
+                        if (p.relu2) {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) {
+                                float x = g[j];
+                                if (p.clamp > 0.0f) x = clamp_nan(x, p.clamp);
+                                const float r = x > 0.0f || x != x ? x : 0.0f;  // a NaN row stays NaN
+                                float hv = r * r;
+                                if (p.route_probs != nullptr) hv *= __shfl_sync(0xffffffffu, pv, j);
+                                *reinterpret_cast<__nv_bfloat16*>(tbuf + j * 64 + lane * 2) = __float2bfloat16_rn(hv);
+                            }
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const int r = i * 8 + (lane >> 2);
+                                const int route = c * 32 + r;
+                                const uint4 w = *reinterpret_cast<const uint4*>(tbuf + r * 64 + (lane & 3) * 16);
+                                if (route < ti.z && f0 + (lane & 3) * 8 < p.out_cols)
+                                    *reinterpret_cast<uint4*>(h + (size_t)(ti.y + route) * (size_t)p.out_ld + f0 +
+                                                              (lane & 3) * 8) = w;
+                            }
+                        } else {
+                            // lanes < 16 keep the gate values of routes 0..15 and receive the up values;
+                            // lanes >= 16 keep the up values of routes 16..31 and receive the gate values
+                            uint8_t* row0 = tbuf + (lo ? 0 : 16 * 32 + 64) + (lane & 15) * 2;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float mine = lo ? g[j] : g[16 + j];
+                                const float other = __shfl_xor_sync(0xffffffffu, lo ? g[16 + j] : g[j], 16);
+                                float hv = swiglu_value(lo ? mine : other, lo ? other : mine, p.clamp);
+                                if (p.route_probs != nullptr) hv *= __shfl_sync(0xffffffffu, pv, lo ? j : 16 + j);
+                                *reinterpret_cast<__nv_bfloat16*>(row0 + j * 32) = __float2bfloat16_rn(hv);
+                            }
+                            __syncwarp();
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const int r = i * 16 + (lane >> 1);
+                                const int route = c * 32 + r;
+                                const uint4 w = *reinterpret_cast<const uint4*>(tbuf + r * 32 + (r >= 16 ? 64 : 0) +
+                                                                                (lane & 1) * 16);
+                                if (route < ti.z)
+                                    *reinterpret_cast<uint4*>(h + (size_t)(ti.y + route) * (size_t)p.out_ld + f0 +
+                                                              (lane & 1) * 8) = w;
+                            }
+                        }
+                        __syncwarp();
+                    }
+                }
+            } else if (w0 < p.out_cols) {
+                // transpose the int32 sums; a lane then holds 8 (bf16) or 4 (fp32) columns of a row
+                const bool bf16 = kMode == kDense && p.out_bf16 != 0;
+                const int cl = bf16 ? (lane & 3) * 8 : (lane & 7) * 4;  // the lane's first column of 32
+                const float* wsp = p.w_scale + (kMode == kDense ? 0 : (size_t)ti.x * p.a_rows) + w0 + cl;
+                float wsr[8];
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    wsr[q] = (q < 4 || bf16) && w0 + cl + q < p.out_cols ? __ldg(wsp + q) : 0.0f;
+                const float4 ws0 = make_float4(wsr[0], wsr[1], wsr[2], wsr[3]);
+                const float4 ws1 = make_float4(wsr[4], wsr[5], wsr[6], wsr[7]);
+                // whole 16-byte stores: every lane column group inside out, rows 16-byte aligned
+                const bool wide = kMode == kDown ||
+                                  (p.out_ld % (bf16 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0);
+                const int valid = p.out_cols - w0 - cl;  // columns of this lane inside out (may be <= 0 or > 8)
+#pragma unroll 1
+                for (int c = half; c < nch; c += 2) {
+                    uint32_t v[32];
+                    tmem_ld_32x32b_x32(taddr + c * 32, v);
+                    s_xs[lane] = c * 32 + lane < ti.z ? __ldg(p.row_scale + ti.y + c * 32 + lane) : 0.0f;
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int r = 0; r < 32; ++r) *reinterpret_cast<uint32_t*>(tbuf + r * 128 + lane * 4) = v[r];
+                    __syncwarp();
+                    if (bf16) {
+                        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int r = i * 8 + (lane >> 2);
+                            const int row = c * 32 + r;
+                            const int4 v0 = *reinterpret_cast<const int4*>(tbuf + r * 128 + cl * 4);
+                            const int4 v1 = *reinterpret_cast<const int4*>(tbuf + r * 128 + cl * 4 + 16);
+                            const float xs = s_xs[r];
+                            const float4 a = scaled4(v0, xs, ws0), b = scaled4(v1, xs, ws1);
+                            const uint4 w = make_uint4(bf16x2(a.x, a.y), bf16x2(a.z, a.w), bf16x2(b.x, b.y),
+                                                       bf16x2(b.z, b.w));
+                            if (row >= ti.z) continue;
+                            __nv_bfloat16* dst = out + (size_t)(ti.y + row) * (size_t)p.out_ld + w0 + cl;
+                            if (wide && valid >= 8) {
+                                *reinterpret_cast<uint4*>(dst) = w;
+                            } else {
+                                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                for (int q = 0; q < 8; ++q)
+                                    if (q < valid)
+                                        reinterpret_cast<uint16_t*>(dst)[q] = (uint16_t)(ww[q >> 1] >> (16 * (q & 1)));
+                            }
+                        }
+                    } else {
+                        float* out = reinterpret_cast<float*>(p.out);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = i * 4 + (lane >> 3);
+                            const int row = c * 32 + r;
+                            const float4 a = scaled4(*reinterpret_cast<const int4*>(tbuf + r * 128 + cl * 4), s_xs[r],
+                                                     ws0);
+                            if (row >= ti.z) continue;
+                            float* dst = out + (size_t)(ti.y + row) * (size_t)p.out_ld + w0 + cl;
+                            if (wide && valid >= 4) {
+                                *reinterpret_cast<float4*>(dst) = a;
+                            } else {
+                                const float aa[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)
+                                    if (q < valid) dst[q] = aa[q];
+                            }
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_empty0[buf]);  // release on CTA 0's barrier
+        }
+    }
+
+    // ---------------- teardown: no pair MMA is in flight once CTA 0 has seen "done"
+    tc_fence_before_sync();
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc_pair(tmem_base, kTmemCols);
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    moe_gemm_gate_up_swiglu_int8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BoxMaps8 tmB,
+                                 const Int8Gemm p) {
+    int8_gemm_body<kGateUp>(tmA, &tmB, p);
+}
+__global__ void __launch_bounds__(kThreads, 1)
+    moe_gemm_down_int8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BoxMaps8 tmB,
+                       const Int8Gemm p) {
+    int8_gemm_body<kDown>(tmA, &tmB, p);
+}
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_dense_int8(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ BoxMaps8 tmB, const Int8Gemm p) {
+    int8_gemm_body<kDense>(tmA, &tmB, p);
+}
+
+typedef void (*GemmKernel)(CUtensorMap, BoxMaps8, Int8Gemm);
+
+cudaError_t launch_pair(GemmKernel kern, int which, const CUtensorMap& a, const BoxMaps8& b, const Int8Gemm& g,
+                        long long max_tiles, cudaStream_t s) {
+    constexpr int kDevices = 64;
+    static int resident[3][kDevices];  // pairs that can be resident, per kernel and device (0: not asked yet)
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see pdl_wait()
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (resident[which][dev] == 0) {
+        err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+        if (err != cudaSuccess) return err;
+        int clusters = 0;
+        cfg.gridDim = dim3(2 * (num_sms() / 2));
+        err = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg);
+        if (err != cudaSuccess) return err;
+        if (clusters < 1) return cudaErrorInvalidConfiguration;
+        resident[which][dev] = clusters < num_sms() / 2 ? clusters : num_sms() / 2;
+    }
+    long long pairs = resident[which][dev];
+    if (pairs > max_tiles) pairs = max_tiles;
+    if (pairs < 1) pairs = 1;
+    cfg.gridDim = dim3((unsigned)(2 * pairs));
+    cfg.numAttrs = 2;
+    err = cudaLaunchKernelEx(&cfg, kern, a, b, g);
+    if (err != cudaSuccess) return err;
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gemm1_int8(const CUtensorMap& a, const BoxMaps8& b, const Int8Gemm& g, long long max_tiles,
+                              cudaStream_t s) {
+    return launch_pair(moe_gemm_gate_up_swiglu_int8, kGateUp, a, b, g, max_tiles, s);
+}
+cudaError_t launch_gemm2_int8(const CUtensorMap& a, const BoxMaps8& b, const Int8Gemm& g, long long max_tiles,
+                              cudaStream_t s) {
+    return launch_pair(moe_gemm_down_int8, kDown, a, b, g, max_tiles, s);
+}
+cudaError_t launch_gemm_dense_int8(const CUtensorMap& a, const BoxMaps8& b, const Int8Gemm& g, long long max_tiles,
+                                   cudaStream_t s) {
+    return launch_pair(gemm_dense_int8, kDense, a, b, g, max_tiles, s);
+}
+
+}  // namespace moe

@@ -1,0 +1,337 @@
+// int8.cu -- the 8-bit integer precision's quantisers: rows of bf16 through the
+// public entry point, token rows of x into their padded route rows, the bf16 h
+// rows of the gate/up GEMM, and the expert weights into the GEMMs' layout (the
+// arithmetic is in int8.cuh); and the dense product's entry points.
+//
+// Layout of the expert weights: blocks of 16 KB, one per (expert, 128 weight
+// rows, 128 elements of K), [128 rows][128 codes], the blocks of one row block
+// after one another along K, so that a pipeline stage of two blocks is one
+// 32 KB run of memory.  W1's rows interleave gate and up in groups of 16 as the
+// bf16 weights do; padding (K past H or F, rows past F or H) holds code 0 and
+// scale 0.  Each weight row's scale stands at the row's own place in [E][rows].
+#include <cmath>
+
+#include "int8.cuh"
+#include "mxfp8.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kI8Threads = 128;
+
+__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
+    f[0] = bf16lo(v.x); f[1] = bf16hi(v.x); f[2] = bf16lo(v.y); f[3] = bf16hi(v.y);
+    f[4] = bf16lo(v.z); f[5] = bf16hi(v.z); f[6] = bf16lo(v.w); f[7] = bf16hi(v.w);
+}
+// The largest magnitude of eight bf16 as bits: |v|'s bits order as its value, infinities and
+// NaN above every number.
+__device__ __forceinline__ uint32_t amax_bits(uint4 v, uint32_t a) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        a = max(a, (w[i] << 16) & 0x7fffffffu);
+        a = max(a, w[i] & 0x7fff0000u);
+    }
+    return a;
+}
+// fmaxf-like in bits: a NaN among them stays the largest, and int8_scale takes it for what it is.
+__device__ __forceinline__ float amax_of(uint32_t bits) { return __uint_as_float(bits); }
+
+__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
+    return (uint32_t)(a & 255) | ((uint32_t)(b & 255) << 8) | ((uint32_t)(c & 255) << 16) | ((uint32_t)d << 24);
+}
+__device__ __forceinline__ uint2 codes8(uint4 v, float scale) {
+    float f[8];
+    unpack8(v, f);
+    int q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) q[i] = scale == scale ? int8_code(f[i], scale) : 0;
+    return make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+}
+
+__device__ __forceinline__ uint32_t block_max_u32(uint32_t a, uint32_t* s_red) {
+    a = __reduce_max_sync(0xffffffffu, a);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = a;
+    __syncthreads();
+    uint32_t m = 0u;
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) m = max(m, s_red[w]);
+    return m;
+}
+
+// Rows of bf16: a block per row; one pass for the largest magnitude, one for the codes.
+__global__ void __launch_bounds__(kI8Threads) int8_quantize_rows_kernel(const uint4* __restrict__ in, long long rows,
+                                                                        int chunks, long long ld_chunks,
+                                                                        const int* __restrict__ live,
+                                                                        uint2* __restrict__ q,
+                                                                        float* __restrict__ scales) {
+    __shared__ uint32_t s_red[kI8Threads / 32];
+    pdl_trigger();
+    pdl_wait();
+    long long n = rows;
+    if (live != nullptr) {
+        const long long l = (long long)__ldg(live);
+        n = l < 0 ? 0 : (l < rows ? l : rows);
+    }
+    for (long long r = blockIdx.x; r < n; r += gridDim.x) {
+        const uint4* src = in + r * ld_chunks;
+        uint32_t a = 0u;
+        for (int c = threadIdx.x; c < chunks; c += kI8Threads) a = amax_bits(__ldg(src + c), a);
+        const float s = int8_scale(amax_of(block_max_u32(a, s_red)));
+        if (threadIdx.x == 0) scales[r] = s;
+        for (int c = threadIdx.x; c < chunks; c += kI8Threads) q[r * chunks + c] = codes8(__ldg(src + c), s);
+    }
+}
+
+// x rows: a block per token writes the token's codes and scale to each of its k padded route
+// rows (zero codes from H to the pitch hp).
+__global__ void __launch_bounds__(kI8Threads) gather_rows_int8_kernel(const uint4* __restrict__ x,
+                                                                      const int* __restrict__ live, int max_live,
+                                                                      int H, int hp, int k,
+                                                                      const int* __restrict__ inv,
+                                                                      uint2* __restrict__ xq, float* __restrict__ xs,
+                                                                      const unsigned* status) {
+    __shared__ int s_prow[kMaxTopK];
+    __shared__ uint32_t s_red[kI8Threads / 32];
+    pdl_trigger();
+    pdl_wait();
+    const int n = live_rows(live, max_live, status);
+    const int chunks = H / 8, chunks_out = hp / 8;
+    for (int t = blockIdx.x; t < n; t += gridDim.x) {
+        __syncthreads();
+        if (threadIdx.x < k) s_prow[threadIdx.x] = __ldg(inv + (size_t)t * k + threadIdx.x);
+        const uint4* src = x + (size_t)t * chunks;
+        uint32_t a = 0u;
+        for (int c = threadIdx.x; c < chunks; c += kI8Threads) a = amax_bits(__ldg(src + c), a);
+        const float s = int8_scale(amax_of(block_max_u32(a, s_red)));
+        if (threadIdx.x < k && s_prow[threadIdx.x] >= 0) xs[s_prow[threadIdx.x]] = s;
+        for (int c = threadIdx.x; c < chunks_out; c += kI8Threads) {
+            const uint2 codes = c < chunks ? codes8(__ldg(src + c), s) : make_uint2(0u, 0u);
+            for (int j = 0; j < k; ++j) {
+                const int pr = s_prow[j];
+                if (pr >= 0) xq[(size_t)pr * chunks_out + c] = codes;
+            }
+        }
+    }
+}
+
+// h rows: a block per live route quantises its bf16 row of the gate/up GEMM (pitch fp, zeros
+// past F) with the row's own scale.
+__global__ void __launch_bounds__(kI8Threads) quantize_h_int8_kernel(const uint4* __restrict__ h,
+                                                                     const int* __restrict__ live, int max_live,
+                                                                     int k, int fp, const int* __restrict__ inv,
+                                                                     uint2* __restrict__ hq, float* __restrict__ hs,
+                                                                     const unsigned* status) {
+    __shared__ uint32_t s_red[kI8Threads / 32];
+    pdl_trigger();
+    pdl_wait();
+    const int n = live_rows(live, max_live, status);
+    const int chunks = fp / 8;
+    for (long long i = blockIdx.x; i < (long long)n * k; i += gridDim.x) {
+        const int pr = __ldg(inv + i);  // uniform over the block
+        if (pr < 0) continue;
+        const uint4* src = h + (size_t)pr * chunks;
+        uint32_t a = 0u;
+        for (int c = threadIdx.x; c < chunks; c += kI8Threads) a = amax_bits(__ldg(src + c), a);
+        const float s = int8_scale(amax_of(block_max_u32(a, s_red)));
+        if (threadIdx.x == 0) hs[pr] = s;
+        for (int c = threadIdx.x; c < chunks; c += kI8Threads) hq[(size_t)pr * chunks + c] = codes8(__ldg(src + c), s);
+    }
+}
+
+// Weights: a block per weight row, codes in 16 KB blocks (see the header), scale beside.
+__global__ void __launch_bounds__(kI8Threads) prepare_int8_kernel(
+    const uint4* __restrict__ wg, const uint4* __restrict__ wu, const uint4* __restrict__ wd, uint2* __restrict__ w1q,
+    float* __restrict__ w1s, uint2* __restrict__ w2q, float* __restrict__ w2s, int E, int F, int H, int w1r, int hr,
+    int at1, int at2, int relu2) {
+    __shared__ uint32_t s_red[kI8Threads / 32];
+    const long long rows1 = (long long)E * (relu2 ? 1 : 2) * F;
+    const long long rows2 = (long long)E * H;
+    for (long long row = blockIdx.x; row < rows1 + rows2; row += gridDim.x) {
+        const bool first = row < rows1;
+        const uint4* src;
+        long long e;
+        int wrow;  // row within the expert's prepared matrix
+        if (first) {
+            const int per_e = relu2 ? F : 2 * F;
+            e = row / per_e;
+            const int rem = (int)(row - e * per_e);
+            const int gu = rem / F, f = rem - gu * F;
+            src = (gu ? wu : wg) + ((size_t)e * F + f) * (H / 8);
+            wrow = relu2 ? f : (f >> 6) * 128 + ((f >> 4) & 3) * 32 + gu * 16 + (f & 15);
+        } else {
+            const long long r2 = row - rows1;
+            e = r2 / H;
+            wrow = (int)(r2 - e * H);
+            src = wd + (size_t)r2 * (F / 8);
+        }
+        const int chunks = (first ? H : F) / 8, atoms = first ? at1 : at2, per = first ? w1r : hr;
+        uint32_t a = 0u;
+        for (int c = threadIdx.x; c < chunks; c += kI8Threads) a = amax_bits(__ldg(src + c), a);
+        const float s = int8_scale(amax_of(block_max_u32(a, s_red)));
+        const long long grow = e * per + wrow;
+        if (threadIdx.x == 0) (first ? w1s : w2s)[grow] = s;
+        uint2* dst = (first ? w1q : w2q) + ((size_t)(grow >> 7) * atoms * 128 + (grow & 127)) * 16;
+        for (int c = threadIdx.x; c < chunks; c += kI8Threads)
+            dst[(size_t)(c >> 4) * (128 * 16) + (c & 15)] = codes8(__ldg(src + c), s);
+    }
+}
+
+int capped_grid(long long items, int per_sm) {
+    const long long cap = (long long)num_sms() * per_sm;
+    return (int)(items < 1 ? 1 : (items > cap ? cap : items));
+}
+
+bool is_aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+constexpr long long kMaxRowsI8 = 1ll << 24;
+constexpr int kMaxColsI8 = 1 << 20;
+
+// Checks that int8_matmul and int8_linear share (the activations apart).
+moe_status check_product(long long rows, int cols_in, const void* w, const float* w_scales, int cols_out,
+                         const void* out, long long ld_out) {
+    if (w == nullptr || w_scales == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
+    if (rows < 0 || cols_in <= 0 || cols_out <= 0 || ld_out < cols_out) return MOE_ERR_INVALID_ARG;
+    // 131,071 products of -128 * -128 fill an int32 sum
+    if (cols_in % 16 != 0 || cols_in > MOE_INT8_MAX_K || cols_out > kMaxColsI8 || rows > kMaxRowsI8)
+        return MOE_ERR_UNSUPPORTED;
+    if (!is_aligned(w, 16) || !is_aligned(w_scales, 4)) return MOE_ERR_ALIGNMENT;
+    return MOE_OK;
+}
+
+moe_status run_dense(const int8_t* x, const float* x_scales, long long rows, int cols_in, long long ld_x,
+                     const int8_t* w, const float* w_scales, int cols_out, void* out, long long ld_out, int out_bf16,
+                     const int* live, unsigned* status, cudaStream_t s) {
+    CUtensorMap tA;
+    BoxMaps8 tB;
+    // rows of K bytes; columns past K and rows past the last read as zero
+    const unsigned long long dW[2] = {(unsigned long long)cols_in, (unsigned long long)cols_out};
+    const unsigned long long sW[1] = {(unsigned long long)cols_in};
+    const unsigned long long dX[2] = {(unsigned long long)cols_in, (unsigned long long)rows};
+    const unsigned long long sX[1] = {(unsigned long long)ld_x};
+    const unsigned boxW[2] = {128, 128};
+    if (!make_tensor_map(&tA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, w, dW, sW, boxW, CU_TENSOR_MAP_SWIZZLE_128B))
+        return MOE_ERR_CUDA;
+    for (int i = 0; i < 8; ++i) {
+        const unsigned box[2] = {128, 16u * (unsigned)(i + 1)};
+        if (!make_tensor_map(&tB.m[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, x, dX, sX, box, CU_TENSOR_MAP_SWIZZLE_128B))
+            return MOE_ERR_CUDA;
+    }
+    Int8Gemm g{};
+    g.status_flags = status;
+    g.out = out;
+    g.out_ld = ld_out;
+    g.out_cols = cols_out;
+    g.n_tiles = (cols_out + 255) / 256;
+    g.atoms = (cols_in + kAtomK8 - 1) / kAtomK8;
+    g.wait_limit_ns = kWaitLimitNs;
+    g.row_scale = x_scales;
+    g.w_scale = w_scales;
+    g.live = live;
+    g.rows = (int)rows;
+    g.out_bf16 = out_bf16;
+    const long long tiles = (rows + kRouteTile - 1) / kRouteTile * g.n_tiles;
+    return launch_gemm_dense_int8(tA, tB, g, tiles, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+size_t linear_scales_offset(long long rows, int cols_in) {
+    return ((size_t)rows * (size_t)cols_in + 255) & ~size_t(255);
+}
+
+}  // namespace
+
+cudaError_t launch_int8_quantize_rows(const __nv_bfloat16* in, long long rows, int cols, long long ld_in, int8_t* q,
+                                      float* scales, const int* live, cudaStream_t s) {
+    return launch_dependent(int8_quantize_rows_kernel, dim3(capped_grid(rows, 16)), dim3(kI8Threads), 0, s,
+                            reinterpret_cast<const uint4*>(in), rows, cols / 8, ld_in / 8, live,
+                            reinterpret_cast<uint2*>(q), scales);
+}
+
+cudaError_t launch_gather_int8(const __nv_bfloat16* x, const int* live, int max_live, int H, int hp, int k,
+                               const int* inv, uint8_t* xq, float* xs, const unsigned* status, cudaStream_t s) {
+    return launch_dependent(gather_rows_int8_kernel, dim3(capped_grid(max_live, 16)), dim3(kI8Threads), 0, s,
+                            reinterpret_cast<const uint4*>(x), live, max_live, H, hp, k, inv,
+                            reinterpret_cast<uint2*>(xq), xs, status);
+}
+
+cudaError_t launch_quantize_h_int8(const __nv_bfloat16* h, const int* live, int max_live, int k, int fp,
+                                   const int* inv, uint8_t* hq, float* hs, const unsigned* status, cudaStream_t s) {
+    return launch_dependent(quantize_h_int8_kernel, dim3(capped_grid((long long)max_live * k, 16)), dim3(kI8Threads),
+                            0, s, reinterpret_cast<const uint4*>(h), live, max_live, k, fp, inv,
+                            reinterpret_cast<uint2*>(hq), hs, status);
+}
+
+cudaError_t launch_prepare_int8(const moe_plan* p, const __nv_bfloat16* wg, const __nv_bfloat16* wu,
+                                const __nv_bfloat16* wd, void* buf, cudaStream_t s) {
+    uint8_t* base = static_cast<uint8_t*>(buf);
+    const int E = p->d.num_experts, F = p->d.ffn, H = p->d.hidden;
+    const bool relu2 = (p->d.flags & MOE_FLAG_SQUARED_RELU) != 0;
+    // padding codes and scales are zero
+    const cudaError_t err = cudaMemsetAsync(base, 0, p->wb.total, s);
+    if (err != cudaSuccess) return err;
+    prepare_int8_kernel<<<num_sms() * 16, kI8Threads, 0, s>>>(
+        reinterpret_cast<const uint4*>(wg), reinterpret_cast<const uint4*>(wu), reinterpret_cast<const uint4*>(wd),
+        reinterpret_cast<uint2*>(base + p->wb.w1), reinterpret_cast<float*>(base + p->wb.w1s),
+        reinterpret_cast<uint2*>(base + p->wb.w2), reinterpret_cast<float*>(base + p->wb.w2s), E, F, H, (int)p->w1r,
+        (int)p->hr, p->ks1, p->ks2, relu2 ? 1 : 0);
+    return cudaGetLastError();
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status int8_quantize_rows(const void* in, long long rows, int cols, long long ld_in, int8_t* q, float* scales,
+                              const int* live_rows_dev, void* stream) {
+    if (in == nullptr || q == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
+    if (rows < 0 || cols <= 0 || ld_in < cols) return MOE_ERR_INVALID_ARG;
+    if (cols % 8 != 0) return MOE_ERR_UNSUPPORTED;
+    if (ld_in % 8 != 0 || !is_aligned(in, 16) || !is_aligned(q, 8) || !is_aligned(scales, 4)) return MOE_ERR_ALIGNMENT;
+    if (rows == 0) return MOE_OK;
+    const cudaError_t e = launch_int8_quantize_rows(static_cast<const __nv_bfloat16*>(in), rows, cols, ld_in, q, scales,
+                                                    live_rows_dev, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status int8_matmul(const int8_t* x, const float* x_scales, long long rows, int cols_in, long long ld_x,
+                       const int8_t* w, const float* w_scales, int cols_out, void* out, long long ld_out,
+                       int out_bf16, const int* live_rows_dev, unsigned* status_dev, void* stream) {
+    if (x == nullptr || x_scales == nullptr || ld_x < cols_in) return MOE_ERR_INVALID_ARG;
+    const moe_status st = check_product(rows, cols_in, w, w_scales, cols_out, out, ld_out);
+    if (st != MOE_OK) return st;
+    if (ld_x % 16 != 0 || !is_aligned(x, 16) || !is_aligned(x_scales, 4) || !is_aligned(out, out_bf16 ? 2 : 4))
+        return MOE_ERR_ALIGNMENT;
+    if (rows == 0) return MOE_OK;
+    return run_dense(x, x_scales, rows, cols_in, ld_x, w, w_scales, cols_out, out, ld_out, out_bf16, live_rows_dev,
+                     status_dev, static_cast<cudaStream_t>(stream));
+}
+
+size_t int8_linear_workspace_bytes(long long rows, int cols_in) {
+    if (rows < 0 || cols_in <= 0) return 0;
+    return linear_scales_offset(rows, cols_in) + (((size_t)rows * 4 + 255) & ~size_t(255)) + 256;
+}
+
+moe_status int8_linear(const void* x, long long rows, int cols_in, long long ld_x, const int8_t* w,
+                       const float* w_scales, int cols_out, void* out, long long ld_out, int out_bf16,
+                       const int* live_rows_dev, void* workspace, size_t ws_bytes, unsigned* status_dev,
+                       void* stream) {
+    if (x == nullptr || workspace == nullptr || ld_x < cols_in) return MOE_ERR_INVALID_ARG;
+    const moe_status st = check_product(rows, cols_in, w, w_scales, cols_out, out, ld_out);
+    if (st != MOE_OK) return st;
+    if (ws_bytes < int8_linear_workspace_bytes(rows, cols_in)) return MOE_ERR_WORKSPACE_TOO_SMALL;
+    if (ld_x % 8 != 0 || !is_aligned(x, 16) || !is_aligned(workspace, 256) || !is_aligned(out, out_bf16 ? 2 : 4))
+        return MOE_ERR_ALIGNMENT;
+    if (rows == 0) return MOE_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int8_t* q = static_cast<int8_t*>(workspace);
+    float* scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + linear_scales_offset(rows, cols_in));
+    if (launch_int8_quantize_rows(static_cast<const __nv_bfloat16*>(x), rows, cols_in, ld_x, q, scales, live_rows_dev,
+                                  s) != cudaSuccess)
+        return MOE_ERR_CUDA;
+    return run_dense(q, scales, rows, cols_in, cols_in, w, w_scales, cols_out, out, ld_out, out_bf16, live_rows_dev,
+                     status_dev, s);
+}
+
+}  // extern "C"

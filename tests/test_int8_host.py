@@ -1,0 +1,87 @@
+"""Refusals of the 8-bit integer operators: host checks before any launch, no GPU needed."""
+from __future__ import annotations
+
+import ctypes
+
+import pytest
+import torch
+
+import routed_moe_swiglu_b200 as rm
+
+F = ctypes.c_void_p(1 << 20)  # never dereferenced: validation fails first
+
+
+def at(n):
+    return ctypes.c_void_p((1 << 20) + n)
+
+
+def test_int8_plans():
+    def plan(**kw):
+        return rm.moe_plan_create(**dict(dict(hidden=2048, ffn=1024, num_experts=128, top_k=8, capacity=256,
+                                              precision="int8"), **kw))
+
+    p, b = plan(), plan(precision="bf16")
+    assert p.precision == "int8"
+    wb = rm.moe_weight_buffer_bytes(p)  # a byte per weight and a scale per channel
+    assert 3 * 128 * 2048 * 1024 + 128 * 4096 * 4 <= wb < 0.52 * rm.moe_weight_buffer_bytes(b)
+    assert rm.moe_weight_buffer_bytes(plan(squared_relu=True)) < wb
+    assert plan(hidden=2056, ffn=1032).hidden == 2056
+    for kw, code in ((dict(hidden=2052), 2), (dict(ffn=1025), 2), (dict(keep_h_fp32=True), 1), (dict(hidden=16392), 2)):
+        with pytest.raises(rm.MoeError) as e:
+            plan(**kw)
+        assert e.value.code == code, kw
+
+
+def test_quantize_rejects_bad_arguments():
+    def call(x=F, rows=4, cols=64, ld=64, q=F, s=F):
+        return rm.load_library().int8_quantize_rows(x, rows, cols, ld, q, s, None, None)
+
+    for kw in (dict(x=None), dict(q=None), dict(s=None), dict(rows=-1), dict(cols=0), dict(ld=56)):
+        assert call(**kw) == 1, kw
+    assert call(cols=60) == 2
+    for kw in (dict(ld=68), dict(x=at(8)), dict(q=at(4)), dict(s=at(2))):
+        assert call(**kw) == 3, kw
+    assert call(rows=0) == 0
+
+
+def test_products_reject_bad_arguments():
+    lib = rm.load_library()
+    nb = rm.int8_linear_workspace_bytes(4, 64)
+
+    def matmul(x=F, xs=F, rows=4, K=64, ld=64, w=F, ws=F, N=32, out=F, ldo=32, bf16=0):
+        return lib.int8_matmul(x, xs, rows, K, ld, w, ws, N, out, ldo, bf16, None, None, None)
+
+    def linear(x=F, rows=4, K=64, ld=64, w=F, ws=F, N=32, out=F, ldo=32, bf16=0, buf=F, n=nb):
+        return lib.int8_linear(x, rows, K, ld, w, ws, N, out, ldo, bf16, None, buf, n, None, None)
+
+    for call in (matmul, linear):
+        for kw in (dict(x=None), dict(w=None), dict(ws=None), dict(out=None), dict(rows=-1), dict(K=0), dict(N=0),
+                   dict(ld=48), dict(ldo=31)):
+            assert call(**kw) == 1, (call, kw)
+        big = dict(K=rm.MOE_INT8_MAX_K + 16, ld=rm.MOE_INT8_MAX_K + 16)
+        for kw in (dict(K=40, ld=48), big, dict(rows=(1 << 24) + 1), dict(N=(1 << 20) + 1, ldo=(1 << 20) + 1)):
+            assert call(**kw, **({"n": 1 << 60} if call is linear else {})) == 2, (call, kw)
+        for kw in (dict(x=at(8)), dict(w=at(8)), dict(ws=at(2)), dict(out=at(2)), dict(out=at(1), bf16=1), dict(ld=68)):
+            assert call(**kw) == 3, (call, kw)
+        assert call(rows=0, **({"n": 1 << 20} if call is linear else {})) == 0
+    assert matmul(xs=None) == 1 and matmul(ld=72) == 3
+    assert linear(buf=None) == 1 and linear(n=nb - 1) == 4 and linear(buf=at(64)) == 3
+    assert rm.int8_linear_workspace_bytes(-1, 64) == 0 and rm.int8_linear_workspace_bytes(3, 0) == 0
+    assert rm.int8_linear_workspace_bytes(100, 256) >= 100 * 260
+
+
+def test_the_binding_refuses_other_types_and_shapes():
+    i8, bf = torch.int8, torch.bfloat16
+    x, q, s = torch.zeros(4, 64, dtype=bf), torch.zeros(4, 64, dtype=i8), torch.zeros(4)
+    w, ws, out = torch.zeros(32, 64, dtype=i8), torch.zeros(32), torch.zeros(4, 32)
+    buf = torch.zeros(1024, dtype=torch.uint8)
+    for bad in (lambda: rm.int8_quantize_rows(x.float(), q, s), lambda: rm.int8_quantize_rows(x, q[:3], s),
+                lambda: rm.int8_quantize_rows(x, q.to(torch.uint8), s), lambda: rm.int8_quantize_rows(x, q, s[:3]),
+                lambda: rm.int8_quantize_rows(x.T, q, s), lambda: rm.int8_quantize_rows(x, q, s),  # host tensors
+                lambda: rm.int8_matmul(q, s, w[:, :32], ws, out), lambda: rm.int8_matmul(q, s, w, ws[:31], out),
+                lambda: rm.int8_matmul(q, s[:3], w, ws, out), lambda: rm.int8_matmul(q, s, w, ws, out.half()),
+                lambda: rm.int8_matmul(q, s, w, ws, out[:, :31]), lambda: rm.int8_matmul(x, s, w, ws, out),
+                lambda: rm.int8_matmul(q, s, w.T.contiguous().T, ws, out),
+                lambda: rm.int8_linear(q, w, ws, out, buf), lambda: rm.int8_linear(x, w.float(), ws, out, buf)):
+        with pytest.raises(ValueError):
+            bad()
