@@ -153,15 +153,38 @@ def _ptr(t):
         return None
     if not t.is_cuda:
         raise ValueError("routed_moe_swiglu_b200 takes device tensors only")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream):
     import torch
 
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        # the current stream's handle without a Stream object around it (3.5 us less a call)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        return raw(torch.cuda.current_device()) if raw is not None else torch.cuda.current_stream().cuda_stream
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _ptrs(*tensors):
+    """Device pointers of the tensors (None stays None), which must all be on the current device:
+    the kernels are launched there."""
+    import torch
+
+    dev, out = None, []
+    for t in tensors:
+        if t is None:
+            out.append(None)
+            continue
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
+                raise ValueError("routed_moe_swiglu_b200 takes device tensors only")
+            if dev is not None or d != torch.cuda.current_device():
+                raise ValueError(f"a tensor on cuda:{d}: every tensor must be on the current device")
+            dev = d
+        out.append(t.data_ptr())
+    return out
 
 
 def moe_version() -> str:
@@ -280,22 +303,23 @@ MOE_INT8_MAX_K = 131056
 def int8_quantize_rows(x, q, scales, live_rows=None, stream=None) -> None:
     """x bf16 [rows, cols] (row stride in elements a multiple of 8) -> q int8 [rows, cols] with a scale
     for each row, scales fp32 [rows] (include/moe.h)."""
-    _rows_of("x", x, "bfloat16")
-    rows, cols = x.shape
-    _dense("q", q, "int8", (rows, cols))
-    _dense("scales", scales, "float32", (rows,))
-    _check(load_library().int8_quantize_rows(_ptr(x), rows, cols, _ld(x), _ptr(q), _ptr(scales), _ptr(live_rows),
-                                             _stream(stream)), "int8_quantize_rows")
-
-
-def _rows_of(name: str, t, dtype: str) -> None:
-    """`t` must be a matrix of the dtype named whose rows are dense (any row stride)."""
     import torch
 
-    if t.dtype is not getattr(torch, dtype):
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be a matrix with dense rows")
+    _strided("x", x, torch.bfloat16)
+    rows, cols = x.shape
+    _dense("q", q, torch.int8, (rows, cols))
+    _dense("scales", scales, torch.float32, (rows,))
+    _items("live_rows", live_rows, torch.int32, 1)
+    px, pq, ps, live = _ptrs(x, q, scales, live_rows)
+    _check(load_library().int8_quantize_rows(px, rows, cols, _ld(x), pq, ps, live, _stream(stream)),
+           "int8_quantize_rows")
+
+
+def _strided(name: str, t, dtype) -> None:
+    """`t` must be a matrix of this dtype whose rows are dense (any row stride)."""
+    if t.dtype is not dtype or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        raise ValueError(f"{name} must be a {dtype} matrix with dense rows, not {t.dtype} {tuple(t.shape)} with strides "
+                         f"{t.stride()}")
 
 
 def _ld(t) -> int:
@@ -303,28 +327,34 @@ def _ld(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-def _int8_out(x, wq, w_scales, out) -> int:
+def _int8_operands(x, wq, w_scales, out, live_rows, status) -> int:
+    """Checks what the two products share; whether out is bf16."""
     import torch
 
-    N, K = wq.shape
-    _dense("wq", wq, "int8", (N, x.shape[1]))
-    _dense("w_scales", w_scales, "float32", (N,))
+    rows, K = x.shape
+    N = wq.shape[0]
+    _dense("wq", wq, torch.int8, (N, K))
+    _dense("w_scales", w_scales, torch.float32, (N,))
     bf16 = out.dtype is torch.bfloat16
-    _rows_of("out", out, "bfloat16" if bf16 else "float32")
-    if tuple(out.shape) != (x.shape[0], N):
-        raise ValueError(f"out must have shape {(x.shape[0], N)}, not {tuple(out.shape)}")
+    _strided("out", out, torch.bfloat16 if bf16 else torch.float32)
+    if out.shape != (rows, N):
+        raise ValueError(f"out must have shape {(rows, N)}, not {tuple(out.shape)}")
+    _items("live_rows", live_rows, torch.int32, 1)
+    _items("status", status, torch.int32, 1)
     return int(bf16)
 
 
 def int8_matmul(xq, x_scales, wq, w_scales, out, live_rows=None, status=None, stream=None) -> None:
     """out[t, c] = sum_k xq[t, k] * wq[c, k] * x_scales[t] * w_scales[c]: xq int8 [rows, K] (row stride a
     multiple of 16), wq int8 [N, K], out fp32 or bf16 [rows, N] (include/moe.h)."""
-    _rows_of("xq", xq, "int8")
-    bf16 = _int8_out(xq, wq, w_scales, out)
+    import torch
+
+    _strided("xq", xq, torch.int8)
+    bf16 = _int8_operands(xq, wq, w_scales, out, live_rows, status)
     rows, K = xq.shape
-    _dense("x_scales", x_scales, "float32", (rows,))
-    _check(load_library().int8_matmul(_ptr(xq), _ptr(x_scales), rows, K, _ld(xq), _ptr(wq), _ptr(w_scales),
-                                      wq.shape[0], _ptr(out), _ld(out), bf16, _ptr(live_rows), _ptr(status),
+    _dense("x_scales", x_scales, torch.float32, (rows,))
+    px, pxs, pw, pws, po, live, st = _ptrs(xq, x_scales, wq, w_scales, out, live_rows, status)
+    _check(load_library().int8_matmul(px, pxs, rows, K, _ld(xq), pw, pws, wq.shape[0], po, _ld(out), bf16, live, st,
                                       _stream(stream)), "int8_matmul")
 
 
@@ -335,13 +365,14 @@ def int8_linear_workspace_bytes(rows: int, cols_in: int) -> int:
 def int8_linear(x, wq, w_scales, out, workspace, live_rows=None, status=None, stream=None) -> None:
     """int8_matmul of bf16 rows x [rows, K] (row stride a multiple of 8), quantised in the call;
     workspace: int8_linear_workspace_bytes(rows, K) bytes."""
-    _rows_of("x", x, "bfloat16")
-    bf16 = _int8_out(x, wq, w_scales, out)
+    import torch
+
+    _strided("x", x, torch.bfloat16)
+    bf16 = _int8_operands(x, wq, w_scales, out, live_rows, status)
     rows, K = x.shape
-    _check(load_library().int8_linear(_ptr(x), rows, K, _ld(x), _ptr(wq), _ptr(w_scales), wq.shape[0], _ptr(out),
-                                      _ld(out), bf16, _ptr(live_rows), _ptr(workspace),
-                                      workspace.numel() * workspace.element_size(), _ptr(status), _stream(stream)),
-           "int8_linear")
+    px, pw, pws, po, live, ws, st = _ptrs(x, wq, w_scales, out, live_rows, workspace, status)
+    _check(load_library().int8_linear(px, rows, K, _ld(x), pw, pws, wq.shape[0], po, _ld(out), bf16, live, ws,
+                                      workspace.numel() * workspace.element_size(), st, _stream(stream)), "int8_linear")
 
 
 def moe_route_topk(plan: Plan, logits, live_count, ids, probs, stream=None) -> None:
@@ -352,21 +383,26 @@ def moe_route_topk(plan: Plan, logits, live_count, ids, probs, stream=None) -> N
 MOE_MAX_SEQS = 65536
 
 
-def _dense(name: str, t, dtype: str, shape=None, rows=None, cols=None) -> None:
-    """`t` (or None) must be dense, of the dtype named and of `shape`; or, with `rows` and `cols`,
-    of any number of rows from `rows` on and of `cols` columns."""
-    if t is None:
-        return
-    import torch
+def _dense(name: str, t, dtype, shape) -> None:
+    """`t` (or None) must be dense, of this dtype and shape."""
+    if t is not None and (t.dtype is not dtype or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}, not {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
 
-    if t.dtype is not getattr(torch, dtype):
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    got = tuple(t.shape)
-    if (shape is not None and got != shape) or (
-            rows is not None and (len(got) != 2 or got[0] < rows or got[1] != cols)):
-        raise ValueError(f"{name} must have shape {shape or (rows, cols)}, not {got}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+
+def _rows(name: str, t, dtype, rows: int, cols: int) -> None:
+    """`t` (or None) must be a dense matrix of this dtype with `cols` columns and at least `rows` rows."""
+    if t is not None and (t.dtype is not dtype or t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols
+                          or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} matrix of {cols} columns and at least {rows} rows, not "
+                         f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
+
+
+def _items(name: str, t, dtype, count: int) -> None:
+    """`t` (or None) must be dense, of this dtype, with at least `count` elements."""
+    if t is not None and (t.dtype is not dtype or t.numel() < count or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of at least {count} elements, not {t.dtype} "
+                         f"{tuple(t.shape)} with strides {t.stride()}")
 
 
 def moe_balance_workspace_bytes(plan: Plan, num_seqs: int = 1) -> int:
@@ -378,24 +414,25 @@ def moe_balance_loss(plan: Plan, logits, ids, live_count, counts, prob_sums, lse
     """The router's balance and z losses with per-expert counts (include/moe.h).  The number of
     sequences is counts.shape[0]; outputs: counts int32 and prob_sums fp32 [num_seqs, E], lse fp32
     [capacity], losses fp32 [2] (balance, z), grad_scales fp32 [num_seqs + 1] (for moe_route_backward)."""
+    import torch
+
+    f32, i32 = torch.float32, torch.int32
     S, E, k, n = counts.shape[0], plan.num_experts, plan.top_k, plan.max_live_rows
-    _dense("logits", logits, "float32", rows=n, cols=E)
-    _dense("ids", ids, "int32", rows=n, cols=k)
-    _dense("live_count", live_count, "int32")
-    _dense("counts", counts, "int32", (S, E))
-    _dense("prob_sums", prob_sums, "float32", (S, E))
-    _dense("lse", lse, "float32")
-    if lse.numel() < n or (token_mask is not None and token_mask.numel() < n):
-        raise ValueError(f"lse and token_mask must have an element for each of the {n} rows")
-    _dense("losses", losses, "float32", (2,))
-    _dense("grad_scales", grad_scales, "float32", (S + 1,))
-    _dense("token_mask", token_mask, "uint8")
-    _dense("seq_offsets", seq_offsets, "int32", (S + 1,))
-    _check(load_library().moe_balance_loss(plan.handle, _ptr(logits), _ptr(ids), _ptr(token_mask), _ptr(seq_offsets), S,
-                                           float(balance_coef), float(z_coef), _ptr(live_count), _ptr(counts),
-                                           _ptr(prob_sums), _ptr(lse), _ptr(losses), _ptr(grad_scales),
-                                           _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                           _stream(stream)), "moe_balance_loss")
+    _rows("logits", logits, f32, n, E)
+    _rows("ids", ids, i32, n, k)
+    _items("live_count", live_count, i32, 1)
+    _dense("counts", counts, i32, (S, E))
+    _dense("prob_sums", prob_sums, f32, (S, E))
+    _items("lse", lse, f32, n)
+    _dense("losses", losses, f32, (2,))
+    _dense("grad_scales", grad_scales, f32, (S + 1,))
+    _items("token_mask", token_mask, torch.uint8, n)
+    _dense("seq_offsets", seq_offsets, i32, (S + 1,))
+    lg, idp, mask, off, live, cnt, ps, ls, lo, gs, ws = _ptrs(logits, ids, token_mask, seq_offsets, live_count, counts,
+                                                              prob_sums, lse, losses, grad_scales, workspace)
+    _check(load_library().moe_balance_loss(plan.handle, lg, idp, mask, off, S, float(balance_coef), float(z_coef), live, cnt,
+                                           ps, ls, lo, gs, ws, workspace.numel() * workspace.element_size(), _stream(stream)),
+           "moe_balance_loss")
 
 
 def moe_route_backward(plan: Plan, logits, ids, live_count, dlogits, lse=None, counts=None, grad_scales=None,
@@ -403,44 +440,48 @@ def moe_route_backward(plan: Plan, logits, ids, live_count, dlogits, lse=None, c
     """Gradient of the router's logits (include/moe.h): the losses' part from logits, lse, counts and
     grad_scales (as moe_balance_loss left them) and grad_losses fp32 [2] (None: 1, 1); the chosen
     part from ids, probs and dprobs.  Either part may be None."""
+    import torch
+
+    f32, i32 = torch.float32, torch.int32
     E, k, n = plan.num_experts, plan.top_k, plan.max_live_rows
     S = counts.shape[0] if counts is not None else 1
-    _dense("logits", logits, "float32", rows=n, cols=E)
-    _dense("ids", ids, "int32", rows=n, cols=k)
-    _dense("live_count", live_count, "int32")
-    _dense("dlogits", dlogits, "float32", rows=n, cols=E)
-    _dense("lse", lse, "float32")
-    if lse is not None and lse.numel() < n:
-        raise ValueError(f"lse must have an element for each of the {n} rows")
-    _dense("counts", counts, "int32", (S, E))
-    _dense("grad_scales", grad_scales, "float32", (S + 1,))
-    _dense("grad_losses", grad_losses, "float32", (2,))
-    _dense("probs", probs, "float32", rows=n, cols=k)
-    _dense("dprobs", dprobs, "float32", rows=n, cols=k)
     if counts is None:
         seq_offsets = None  # the chosen part knows no sequences
-    _dense("seq_offsets", seq_offsets, "int32", (S + 1,))
-    _check(load_library().moe_route_backward(plan.handle, _ptr(logits), _ptr(ids), _ptr(lse), _ptr(counts),
-                                             _ptr(grad_scales), _ptr(grad_losses), _ptr(probs), _ptr(dprobs),
-                                             _ptr(seq_offsets), S, _ptr(live_count), _ptr(dlogits), _stream(stream)),
-           "moe_route_backward")
+    _rows("logits", logits, f32, n, E)
+    _rows("ids", ids, i32, n, k)
+    _items("live_count", live_count, i32, 1)
+    _rows("dlogits", dlogits, f32, n, E)
+    _items("lse", lse, f32, n)
+    _dense("counts", counts, i32, (S, E))
+    _dense("grad_scales", grad_scales, f32, (S + 1,))
+    _dense("grad_losses", grad_losses, f32, (2,))
+    _rows("probs", probs, f32, n, k)
+    _rows("dprobs", dprobs, f32, n, k)
+    _dense("seq_offsets", seq_offsets, i32, (S + 1,))
+    lg, idp, ls, cnt, gs, gl, pr, dp, off, live, dl = _ptrs(logits, ids, lse, counts, grad_scales, grad_losses, probs,
+                                                            dprobs, seq_offsets, live_count, dlogits)
+    _check(load_library().moe_route_backward(plan.handle, lg, idp, ls, cnt, gs, gl, pr, dp, off, S, live, dl,
+                                             _stream(stream)), "moe_route_backward")
 
 
 def moe_combine_backward(plan: Plan, dout, y_rows, route_rows, route_probs, live_count, dprobs=None, dy_rows=None,
                          stream=None) -> None:
     """Gradient of the combine (include/moe.h): dprobs[t, j] = <dout[t], y_rows[route_rows[t, j]]> and
     dy_rows[route_rows[t, j]] = route_probs[t, j] * dout[t]; either may be None."""
+    import torch
+
+    f32, i32 = torch.float32, torch.int32
     H, k, n = plan.hidden, plan.top_k, plan.max_live_rows
-    _dense("dout", dout, "bfloat16" if plan.out_dtype == "bf16" else "float32", rows=n, cols=H)
-    _dense("y_rows", y_rows, "float32", rows=0, cols=H)
-    _dense("route_rows", route_rows, "int32", rows=n, cols=k)
-    _dense("route_probs", route_probs, "float32", rows=n, cols=k)
-    _dense("live_count", live_count, "int32")
-    _dense("dprobs", dprobs, "float32", rows=n, cols=k)
-    _dense("dy_rows", dy_rows, "float32", rows=0, cols=H)
-    _check(load_library().moe_combine_backward(plan.handle, _ptr(dout), _ptr(y_rows), _ptr(route_rows),
-                                               _ptr(route_probs), _ptr(live_count), _ptr(dprobs), _ptr(dy_rows),
-                                               _stream(stream)), "moe_combine_backward")
+    _rows("dout", dout, torch.bfloat16 if plan.out_dtype == "bf16" else f32, n, H)
+    _rows("y_rows", y_rows, f32, 0, H)
+    _rows("route_rows", route_rows, i32, n, k)
+    _rows("route_probs", route_probs, f32, n, k)
+    _items("live_count", live_count, i32, 1)
+    _rows("dprobs", dprobs, f32, n, k)
+    _rows("dy_rows", dy_rows, f32, 0, H)
+    do, y, rows, pr, live, dp, dy = _ptrs(dout, y_rows, route_rows, route_probs, live_count, dprobs, dy_rows)
+    _check(load_library().moe_combine_backward(plan.handle, do, y, rows, pr, live, dp, dy, _stream(stream)),
+           "moe_combine_backward")
 
 
 def _check_out(plan: Plan, out) -> None:

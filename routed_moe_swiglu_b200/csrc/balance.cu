@@ -28,15 +28,20 @@
 #include <cmath>
 
 #include "moe_internal.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kBalThreads = 256;
+constexpr int kBalThreads = 512;
 constexpr int kBalWarps = kBalThreads / 32;
-constexpr int kBalBlocksPerSm = 4;
+constexpr int kBalSumRows = kBalWarps / 2;  // rows of sums in shared memory: half of the warps add the other half's
+constexpr int kGradThreads = 256;
+constexpr int kGradWarps = kGradThreads / 32;
 constexpr int kFinThreads = 1024;
-constexpr int kFinCols = 32;  // columns of a finishing block: a warp per slot row, a lane per column
+constexpr int kFinWarps = kFinThreads / 32;
+constexpr int kFinCols = 32;  // columns of an item of the finish: a warp per slot row, a lane per column
+constexpr float kLog2e = 1.4426950408889634f;
 
 struct BalanceArgs {
     const float* logits;
@@ -122,21 +127,32 @@ __device__ __forceinline__ void load_row(const float* row, int E, int gl, bool h
     }
 }
 
-// Sums of a block's tokens, one slot for each sequence it meets.
+__device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; 0 for -infinity
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+struct StatsShared {
+    float z[kBalWarps];
+    int n[kBalWarps];
+};
+struct FinishShared {
+    float p[kFinWarps][kFinCols + 1];
+    int c[kFinWarps][kFinCols + 1];
+    double a[kFinWarps], b[kFinWarps];
+    int i[kFinWarps], j[kFinWarps];
+};
+
+// Sums of this block's tokens, one slot for each sequence it meets.  The next token's row is on
+// its way while this one's softmax is computed.
 template <int L, int V, bool kVec>
-__global__ void __launch_bounds__(kBalThreads) balance_stats_kernel(const BalanceArgs a) {
-    extern __shared__ float s_bal[];  // [warps][E] sums, then [E] counts
-    __shared__ float s_z[kBalWarps];
-    __shared__ int s_n[kBalWarps];
-    pdl_trigger();
-    pdl_wait();
+__device__ __forceinline__ void balance_stats(const BalanceArgs& a, int n, float* s_sum, int* s_cnt,
+                                              StatsShared& sh) {
     const int E = a.E, k = a.k;
-    int* s_cnt = reinterpret_cast<int*>(s_bal + kBalWarps * E);
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int gl = lane & (L - 1);
     constexpr int kGroups = 32 / L;  // tokens a warp holds at once
-    const int n = clamp_live(a.live, a.max_live);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
     const int chunk = (n + a.blocks - 1) / a.blocks;
     const int c0 = min(n, (int)blockIdx.x * chunk), c1 = min(n, c0 + chunk);
     if (c0 >= c1) return;
@@ -152,16 +168,23 @@ __global__ void __launch_bounds__(kBalThreads) balance_stats_kernel(const Balanc
         if (t_lo >= t_hi) continue;
         for (int e = threadIdx.x; e < E; e += kBalThreads) s_cnt[e] = 0;
         __syncthreads();
-        float acc[V];
+        float acc[V], next[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] = 0.0f;
         float z = 0.0f;
         int cnt = 0;
-        for (int tw = t_lo + warp * kGroups; tw < t_hi; tw += kBalWarps * kGroups) {
-            const int t = tw + lane / L;
-            const bool have = t < t_hi && (a.mask == nullptr || __ldg(a.mask + t) != 0);
+        constexpr int kStep = kBalWarps * kGroups;
+        int t = t_lo + warp * kGroups + lane / L;
+        auto kept = [&](int tt) { return tt < t_hi && (a.mask == nullptr || __ldg(a.mask + tt) != 0); };
+        bool have_next = kept(t);
+        load_row<L, V, kVec>(a.logits + (size_t)t * E, E, gl, have_next, -INFINITY, next);
+        for (int tw = t_lo + warp * kGroups; tw < t_hi; tw += kStep, t += kStep) {
+            const bool have = have_next;
             float x[V];
-            load_row<L, V, kVec>(a.logits + (size_t)t * E, E, gl, have, -INFINITY, x);
+#pragma unroll
+            for (int v = 0; v < V; ++v) x[v] = next[v];
+            have_next = kept(t + kStep);
+            load_row<L, V, kVec>(a.logits + (size_t)(t + kStep) * E, E, gl, have_next, -INFINITY, next);
             float mx = -INFINITY;
 #pragma unroll
             for (int v = 0; v < V; ++v) mx = fmaxf(mx, x[v]);
@@ -170,16 +193,15 @@ __global__ void __launch_bounds__(kBalThreads) balance_stats_kernel(const Balanc
             float sum = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                x[v] = expf(x[v] - mx);
+                x[v] = exp2_approx((x[v] - mx) * kLog2e);  // the difference first: rows near the type's bounds
                 sum += x[v];
             }
             sum = group_sum<L>(sum);
             const bool counted = have && sum != 0.0f;  // true for NaN: it shows in the losses
-            const float inv = counted ? 1.0f / sum : 0.0f;
+            const float inv = counted ? __frcp_rn(sum) : 0.0f;
             const float lse = counted ? mx + logf(sum) : -INFINITY;
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (counted) acc[v] += x[v] * inv;
+            for (int v = 0; v < V; ++v) acc[v] = fmaf(x[v], inv, acc[v]);  // 0 * 0 where it does not count
             if (t < t_hi && gl == 0) {
                 a.lse[t] = lse;
                 if (counted) {
@@ -193,26 +215,38 @@ __global__ void __launch_bounds__(kBalThreads) balance_stats_kernel(const Balanc
                     if (id >= 0 && id < E) atomicAdd(&s_cnt[id], 1);  // integers: any order
                 }
         }
-        // groups of the warp, then warps in order
+        // groups of the warp, then warps in order: the upper half's rows first go through shared
+        // memory to the lower half, which adds them and leaves its rows there
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
+        for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int o = L; o < 32; o <<= 1) acc[v] += __shfl_xor_sync(0xffffffffu, acc[v], o);
-            const int c = col_of<L, kVec>(v, gl);
-            if (lane < L && c < E) s_bal[warp * E + c] = acc[v];
-        }
         z = group_sum<32>(z);
         cnt = __reduce_add_sync(0xffffffffu, cnt);
         if (lane == 0) {
-            s_z[warp] = z;
-            s_n[warp] = cnt;
+            sh.z[warp] = z;
+            sh.n[warp] = cnt;
         }
+        float* mine = s_sum + (warp & (kBalSumRows - 1)) * E;
+        if (warp >= kBalSumRows && lane < L)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int c = col_of<L, kVec>(v, gl);
+                if (c < E) mine[c] = acc[v];
+            }
+        __syncthreads();
+        if (warp < kBalSumRows && lane < L)
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int c = col_of<L, kVec>(v, gl);
+                if (c < E) mine[c] += acc[v];
+            }
         __syncthreads();
         const size_t slot = (size_t)blockIdx.x + s;
         for (int e = threadIdx.x; e < E; e += kBalThreads) {
             float p = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kBalWarps; ++w) p += s_bal[w * E + e];
+            for (int w = 0; w < kBalSumRows; ++w) p += s_sum[w * E + e];
             a.slot_p[slot * E + e] = p;
             a.slot_c[slot * E + e] = s_cnt[e];
         }
@@ -220,8 +254,8 @@ __global__ void __launch_bounds__(kBalThreads) balance_stats_kernel(const Balanc
             float zs = 0.0f;
             int ns = 0;
             for (int w = 0; w < kBalWarps; ++w) {
-                zs += s_z[w];
-                ns += s_n[w];
+                zs += sh.z[w];
+                ns += sh.n[w];
             }
             a.slot_z[slot] = zs;
             a.slot_n[slot] = ns;
@@ -230,24 +264,14 @@ __global__ void __launch_bounds__(kBalThreads) balance_stats_kernel(const Balanc
     }
 }
 
-// Adds the slots of sequence blockIdx.y for 32 experts; the last block to finish
-// turns the sequences' sums into the losses and the gradient's factors.
-__global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const BalanceArgs a) {
-    __shared__ float s_p[kFinThreads / 32][kFinCols + 1];
-    __shared__ int s_c[kFinThreads / 32][kFinCols + 1];
-    __shared__ double s_a[kFinThreads / 32], s_b[kFinThreads / 32];
-    __shared__ int s_i[kFinThreads / 32], s_j[kFinThreads / 32];
-    __shared__ int s_last;
-    pdl_trigger();
-    pdl_wait();
+// Adds the slots of a sequence for 32 experts; `item` is one (sequence, 32 experts) of the
+// num_seqs * ceil(E / 32) that `size` blocks share.
+__device__ __forceinline__ void finish_items(const BalanceArgs& a, int n, int rank, int size, FinishShared& sh) {
     const int E = a.E, S = a.num_seqs;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    constexpr int kWarps = kFinThreads / 32;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int col_blocks = (E + kFinCols - 1) / kFinCols;
-    const int n = clamp_live(a.live, a.max_live);
     const int chunk = (n + a.blocks - 1) / a.blocks;
-    const int items = S * col_blocks;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+    for (int it = rank; it < S * col_blocks; it += size) {
         const int s = it / col_blocks, cb = it - s * col_blocks;
         const int e = cb * kFinCols + lane;
         const int sb = seq_begin(a.seq_off, s, n), se = seq_begin(a.seq_off, s + 1, n);
@@ -256,21 +280,22 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const Balan
         float p = 0.0f;
         int c = 0;
         if (e < E)
-#pragma unroll 4
-            for (int b = b0 + warp; b < b1; b += kWarps) {
+#pragma unroll 8
+            for (int b = b0 + warp; b < b1; b += warps) {
                 const size_t at = (size_t)(b + s) * E + e;
-                p += __ldg(a.slot_p + at);
-                c += __ldg(a.slot_c + at);
+                p += __ldcg(a.slot_p + at);
+                c += __ldcg(a.slot_c + at);
             }
-        s_p[warp][lane] = p;
-        s_c[warp][lane] = c;
+        sh.p[warp][lane] = p;
+        sh.c[warp][lane] = c;
         __syncthreads();
         if (warp == 0) {
             p = 0.0f;
             c = 0;
-            for (int w = 0; w < kWarps; ++w) {
-                p += s_p[w][lane];
-                c += s_c[w][lane];
+#pragma unroll 8
+            for (int w = 0; w < warps; ++w) {
+                p += sh.p[w][lane];
+                c += sh.c[w][lane];
             }
             if (e < E) {
                 a.prob_sums[(size_t)s * E + e] = p;
@@ -283,8 +308,8 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const Balan
             float z = 0.0f;
             int m = 0;
             for (int b = b0 + lane; b < b1; b += 32) {
-                z += __ldg(a.slot_z + b + s);
-                m += __ldg(a.slot_n + b + s);
+                z += __ldcg(a.slot_z + b + s);
+                m += __ldcg(a.slot_n + b + s);
             }
             z = group_sum<32>(z);
             m = __reduce_add_sync(0xffffffffu, m);
@@ -295,17 +320,16 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const Balan
         }
         __syncthreads();
     }
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) s_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1 ? 1 : 0;
-    __syncthreads();
-    if (!s_last) return;
-    __threadfence();
-    // the last block: S', T and the z sum, then the sequences' factors and losses; each thread
-    // takes every kFinThreads-th sequence, and the threads' sums are added in a fixed order
+}
+
+// One block: S', T and the z sum, then the sequences' factors and the losses.  Each thread takes
+// every blockDim-th sequence, and the threads' sums are added in a fixed order.
+__device__ __forceinline__ void finish_total(const BalanceArgs& a, FinishShared& sh) {
+    const int S = a.num_seqs, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int col_blocks = (a.E + kFinCols - 1) / kFinCols;
     int filled = 0, total = 0;
     double z = 0.0;
-    for (int s = threadIdx.x; s < S; s += kFinThreads) {
+    for (int s = threadIdx.x; s < S; s += blockDim.x) {
         const int m = __ldcg(a.seq_n + s);
         filled += m > 0;
         total += m;
@@ -316,22 +340,23 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const Balan
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
     if (lane == 0) {
-        s_i[warp] = filled;
-        s_j[warp] = total;
-        s_b[warp] = z;
+        sh.i[warp] = filled;
+        sh.j[warp] = total;
+        sh.b[warp] = z;
     }
     __syncthreads();
     filled = total = 0;
     z = 0.0;
-    for (int w = 0; w < kWarps; ++w) {
-        filled += s_i[w];
-        total += s_j[w];
-        z += s_b[w];
+    const int used = min(warps, (S + 31) / 32);  // the other warps' sums are 0
+    for (int w = 0; w < used; ++w) {
+        filled += sh.i[w];
+        total += sh.j[w];
+        z += sh.b[w];
     }
     double loss = 0.0;
-    for (int s = threadIdx.x; s < S; s += kFinThreads) {
+    for (int s = threadIdx.x; s < S; s += blockDim.x) {
         const double m = (double)__ldcg(a.seq_n + s);
-        const double as = m > 0.0 ? (double)a.balance_coef * E / ((double)filled * a.k * m * m) : 0.0;
+        const double as = m > 0.0 ? (double)a.balance_coef * a.E / ((double)filled * a.k * m * m) : 0.0;
         double dot = 0.0;
         for (int cb = 0; cb < col_blocks; ++cb) dot += (double)__ldcg(a.seq_dot + (size_t)s * col_blocks + cb);
         if (m > 0.0) loss += as * dot;
@@ -339,16 +364,51 @@ __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const Balan
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
-    if (lane == 0) s_a[warp] = loss;
+    if (lane == 0) sh.a[warp] = loss;
     __syncthreads();
     if (threadIdx.x == 0) {
         loss = 0.0;
-        for (int w = 0; w < kWarps; ++w) loss += s_a[w];
+        for (int w = 0; w < used; ++w) loss += sh.a[w];
         const double zt = total > 0 ? (double)a.z_coef / total : 0.0;
         a.losses[0] = (float)loss;
         a.losses[1] = (float)(total > 0 ? zt * z : 0.0);
         a.grad_scales[S] = (float)(2.0 * zt);
     }
+}
+
+// kOne: the grid is one cluster, which meets in its own barrier between the sums, the finish and
+// the totals; else balance_finish_kernel does the rest.
+template <int L, int V, bool kVec, bool kOne>
+__global__ void __launch_bounds__(kBalThreads, 1) balance_stats_kernel(const BalanceArgs a) {
+    extern __shared__ float s_bal[];  // [kBalSumRows][E] sums, then [E] counts
+    __shared__ StatsShared sh;
+    pdl_trigger();
+    pdl_wait();
+    const int n = clamp_live(a.live, a.max_live);
+    if (!kOne && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
+    balance_stats<L, V, kVec>(a, n, s_bal, reinterpret_cast<int*>(s_bal + kBalSumRows * a.E), sh);
+    if constexpr (kOne) {
+        __shared__ FinishShared fin;
+        cluster_sync();  // the slots of every block are written
+        finish_items(a, n, blockIdx.x, gridDim.x, fin);
+        cluster_sync();
+        if (blockIdx.x == 0) finish_total(a, fin);
+    }
+}
+
+__global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const BalanceArgs a) {
+    __shared__ FinishShared fin;
+    __shared__ int s_last;
+    pdl_trigger();
+    pdl_wait();
+    finish_items(a, clamp_live(a.live, a.max_live), blockIdx.x, gridDim.x, fin);
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) s_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1 ? 1 : 0;
+    __syncthreads();
+    if (!s_last) return;  // the last block to finish has every sequence's sums
+    __threadfence();
+    finish_total(a, fin);
 }
 
 struct RouteGradArgs {
@@ -367,13 +427,14 @@ struct RouteGradArgs {
 };
 
 // A group of lanes per token, as the forward: the losses' part in registers; the chosen part
-// is added to the row in shared memory, from where the whole row leaves in wide stores.
+// is added to the row in shared memory, in route order (an expert named twice gets both adds in
+// that order), from where the whole row leaves in wide stores.  Route j of a token belongs to
+// lane j % L of its group.
 template <int L, int V, bool kVec>
-__global__ void __launch_bounds__(kBalThreads) route_backward_kernel(const RouteGradArgs a) {
+__global__ void __launch_bounds__(kGradThreads) route_backward_kernel(const RouteGradArgs a) {
     extern __shared__ __align__(16) float s_row_all[];
     constexpr int kGroups = 32 / L;
-    __shared__ int s_id[kBalWarps * kGroups][kMaxTopK];
-    __shared__ float s_v[kBalWarps * kGroups][kMaxTopK];
+    constexpr int kSlots = (kMaxTopK + L - 1) / L;  // routes of a lane
     pdl_trigger();
     pdl_wait();
     const int E = a.E, k = a.k;
@@ -393,14 +454,44 @@ __global__ void __launch_bounds__(kBalThreads) route_backward_kernel(const Route
 
     const int chunk = (n + a.blocks - 1) / a.blocks;
     const int c0 = min(n, (int)blockIdx.x * chunk), c1 = min(n, c0 + chunk);
-    for (int tw = c0 + warp * kGroups; tw < c1; tw += kBalWarps * kGroups) {
-        const int t = tw + lane / L;
+    constexpr int kStep = kGradWarps * kGroups;
+    int t = c0 + warp * kGroups + lane / L;
+    auto lse_of = [&](int tt) {
+        return tt < c1 ? (a.lse != nullptr ? __ldg(a.lse + tt) : 0.0f) : -INFINITY;
+    };
+    float lse_next = lse_of(t);
+    float next[V];
+    if (has_loss) load_row<L, V, kVec>(a.logits + (size_t)t * E, E, gl, t < c1, -INFINITY, next);
+    for (int tw = c0 + warp * kGroups; tw < c1; tw += kStep, t += kStep) {
         const bool in = t < c1;
-        const float lse = in && a.lse != nullptr ? __ldg(a.lse + t) : (in ? 0.0f : -INFINITY);
+        const float lse = lse_next;
         const bool counted = lse != -INFINITY;  // true for NaN
         float x[V];
         if (has_loss) {
-            load_row<L, V, kVec>(a.logits + (size_t)t * E, E, gl, counted, -INFINITY, x);
+#pragma unroll
+            for (int v = 0; v < V; ++v) x[v] = next[v];
+        }
+        // the next token's row and this one's routes are on their way meanwhile
+        lse_next = lse_of(t + kStep);
+        if (has_loss)
+            load_row<L, V, kVec>(a.logits + (size_t)(t + kStep) * E, E, gl, t + kStep < c1, -INFINITY, next);
+        int id[kSlots];
+        float w[kSlots], d[kSlots];
+        if (a.dprobs != nullptr) {
+#pragma unroll
+            for (int r = 0; r < kSlots; ++r) {
+                const int j = r * L + gl;
+                const bool on = counted && j < k;
+                id[r] = on ? __ldg(a.ids + (size_t)t * k + j) : -1;
+                w[r] = on ? __ldg(a.probs + (size_t)t * k + j) : 0.0f;
+                d[r] = on ? __ldg(a.dprobs + (size_t)t * k + j) : 0.0f;
+                if (id[r] < 0 || id[r] >= E) {
+                    id[r] = -1;
+                    w[r] = d[r] = 0.0f;
+                }
+            }
+        }
+        if (has_loss) {
             if (counted && (t < s_lo || t >= s_hi)) {
                 int s = find_seq(a.seq_off, a.num_seqs, t);
                 s = s < a.num_seqs ? s : a.num_seqs - 1;
@@ -413,53 +504,69 @@ __global__ void __launch_bounds__(kBalThreads) route_backward_kernel(const Route
                     cnt[v] = c < E ? (float)__ldg(a.counts + (size_t)s * E + c) : 0.0f;
                 }
             }
-            float dot = 0.0f;
+            // p from the row's own maximum and sum: lse has lost the sum where it is large
+            float mx = -INFINITY;
+#pragma unroll
+            for (int v = 0; v < V; ++v) mx = fmaxf(mx, x[v]);
+            mx = group_max<L>(mx);
+            float sum = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                x[v] = counted ? expf(x[v] - lse) : 0.0f;
-                dot += cnt[v] * x[v];
+                x[v] = exp2_approx((x[v] - mx) * kLog2e);
+                sum += x[v];
+                dot = fmaf(cnt[v], x[v], dot);
             }
+            sum = group_sum<L>(sum);
             dot = group_sum<L>(dot);
+            const float inv = __frcp_rn(sum);
+            const float base = fmaf(zs, lse, -as * (dot * inv));  // as * (c - <c, p>) + zs * lse
 #pragma unroll
-            for (int v = 0; v < V; ++v) x[v] = counted ? x[v] * (as * (cnt[v] - dot) + zs * lse) : 0.0f;
+            for (int v = 0; v < V; ++v) x[v] = counted ? x[v] * inv * fmaf(as, cnt[v], base) : 0.0f;
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v) x[v] = 0.0f;
         }
         if (a.dprobs != nullptr) {
+            float wd = 0.0f;
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = col_of<L, kVec>(v, gl);
-                if (c < E) s_row[c] = x[v];
-            }
-            for (int j = gl; j < k; j += L) {
-                const int id = counted ? __ldg(a.ids + (size_t)t * k + j) : -1;
-                const bool ok = id >= 0 && id < E;
-                s_id[g][j] = ok ? id : -1;
-                s_v[g][j] = ok ? __ldg(a.dprobs + (size_t)t * k + j) : 0.0f;
+            for (int r = 0; r < kSlots; ++r) wd = fmaf(w[r], d[r], wd);
+            wd = group_sum<L>(wd);
+            if (kVec) {
+#pragma unroll
+                for (int q = 0; q < V / 4; ++q) {
+                    const int c = q * (4 * L) + gl * 4;
+                    if (c < E)
+                        *reinterpret_cast<float4*>(s_row + c) = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2],
+                                                                            x[4 * q + 3]);
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    if (v * L + gl < E) s_row[v * L + gl] = x[v];
             }
             __syncwarp();
-            float wd = 0.0f;  // <w, d> over the valid routes, in route order
-            for (int j = 0; j < k; ++j)
-                if (s_id[g][j] >= 0) wd += __ldg(a.probs + (size_t)t * k + j) * s_v[g][j];
-            for (int j = gl; j < k; j += L) {
-                const int id = s_id[g][j];
-                if (id < 0) continue;
-                // an expert named twice: its first route adds for all, in route order
-                float add = 0.0f;
-                bool first = true;
-                for (int i = 0; i < k; ++i)
-                    if (s_id[g][i] == id) {
-                        if (i < j) first = false;
-                        add += __ldg(a.probs + (size_t)t * k + i) * (s_v[g][i] - wd);
+#pragma unroll
+            for (int r = 0; r < kSlots; ++r)
+                for (int j = r * L; j < min(k, r * L + L); ++j) {
+                    if (gl == j - r * L && id[r] >= 0) s_row[id[r]] += w[r] * (d[r] - wd);
+                    __syncwarp();
+                }
+            if (kVec) {
+#pragma unroll
+                for (int q = 0; q < V / 4; ++q) {
+                    const int c = q * (4 * L) + gl * 4;
+                    if (c < E) {
+                        const float4 f = *reinterpret_cast<const float4*>(s_row + c);
+                        x[4 * q] = f.x;
+                        x[4 * q + 1] = f.y;
+                        x[4 * q + 2] = f.z;
+                        x[4 * q + 3] = f.w;
                     }
-                if (first) s_row[id] += add;
-            }
-            __syncwarp();
+                }
+            } else {
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = col_of<L, kVec>(v, gl);
-                if (c < E) x[v] = s_row[c];
+                for (int v = 0; v < V; ++v)
+                    if (v * L + gl < E) x[v] = s_row[v * L + gl];
             }
             __syncwarp();
         }
@@ -475,31 +582,39 @@ __global__ void __launch_bounds__(kBalThreads) route_backward_kernel(const Route
                 }
             } else {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    const int c = v * L + gl;
-                    if (c < E) out[c] = x[v];
-                }
+                for (int v = 0; v < V; ++v)
+                    if (v * L + gl < E) out[v * L + gl] = x[v];
             }
         }
     }
 }
 
-int balance_blocks(long long max_live) {
-    const long long cap = (long long)num_sms() * kBalBlocksPerSm;
-    const long long want = (max_live + 15) / 16;
+// Tokens that a warp holds at once (32 / L, as by_width picks L).
+int tokens_per_warp(int E) { return E <= 16 ? 8 : E <= 128 ? 4 : E <= 256 ? 2 : 1; }
+
+int blocks_for(long long max_live, int tokens, long long cap) {
+    const long long want = (max_live + tokens - 1) / tokens;
     return (int)(want < 1 ? 1 : (want > cap ? cap : want));
 }
 
-// The workspace's rows for the largest grid this device or any other can ask for.
-constexpr int kMaxBalBlocks = 1024;
+// Up to this many blocks are one cluster (of a power of two) and one launch.
+constexpr int kClusterBlocks = 8;
+// The workspace has rows for the largest grid any device may ask for.
+constexpr int kMaxBalBlocks = 256;
+
+// Blocks of the sums: one pass of each block's warps at least, `cap` at most.
+int balance_blocks(long long max_live, int E, long long cap) {
+    const int b = blocks_for(max_live, kBalWarps * tokens_per_warp(E), cap);
+    if (b > kClusterBlocks) return b;
+    return b > 4 ? 8 : b > 2 ? 4 : b;
+}
 
 struct BalanceLayout {
     size_t p, c, z, n, dot, sz, sn, ticket, total;
 };
 BalanceLayout balance_layout(const moe_plan* plan, int num_seqs) {
     const size_t E = (size_t)plan->d.num_experts, S = (size_t)num_seqs;
-    long long b = (plan->max_live + 15) / 16;
-    if (b > kMaxBalBlocks) b = kMaxBalBlocks;
+    const int b = balance_blocks(plan->max_live, plan->d.num_experts, kMaxBalBlocks);
     const size_t slots = (size_t)b + S;
     BalanceLayout l;
     size_t off = 0;
@@ -539,15 +654,32 @@ cudaError_t by_width(int E, bool vec, const Args& a, cudaStream_t s) {
 template <int L, int V, bool kVec>
 struct LaunchStats {
     static cudaError_t go(const BalanceArgs& a, cudaStream_t s) {
-        const size_t smem = (size_t)(kBalWarps + 1) * a.E * 4;  // at most 36 KB
-        return launch_dependent(balance_stats_kernel<L, V, kVec>, dim3(a.blocks), dim3(kBalThreads), smem, s, a);
+        const size_t smem = (size_t)(kBalSumRows + 1) * a.E * 4;  // at most 36 KB
+        if (a.blocks > kClusterBlocks)
+            return launch_dependent(balance_stats_kernel<L, V, kVec, false>, dim3(a.blocks), dim3(kBalThreads), smem, s,
+                                    a);
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = (unsigned)a.blocks;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[1].val.programmaticStreamSerializationAllowed = 1;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(a.blocks);
+        cfg.blockDim = dim3(kBalThreads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        const cudaError_t err = cudaLaunchKernelEx(&cfg, balance_stats_kernel<L, V, kVec, true>, a);
+        return err != cudaSuccess ? err : cudaGetLastError();
     }
 };
 template <int L, int V, bool kVec>
 struct LaunchBackward {
     static cudaError_t go(const RouteGradArgs& a, cudaStream_t s) {
-        const size_t smem = a.dprobs != nullptr ? (size_t)kBalWarps * (32 / L) * ((a.E + 3) & ~3) * 4 : 0;  // <= 32 KB
-        return launch_dependent(route_backward_kernel<L, V, kVec>, dim3(a.blocks), dim3(kBalThreads), smem, s, a);
+        const size_t smem = a.dprobs != nullptr ? (size_t)kGradWarps * (32 / L) * ((a.E + 3) & ~3) * 4 : 0;  // <= 32 KB
+        return launch_dependent(route_backward_kernel<L, V, kVec>, dim3(a.blocks), dim3(kGradThreads), smem, s, a);
     }
 };
 
@@ -588,8 +720,7 @@ moe_status moe_balance_loss(const moe_plan* plan, const float* logits, const int
     a.E = plan->d.num_experts;
     a.k = plan->d.top_k;
     a.num_seqs = num_seqs;
-    a.blocks = balance_blocks(plan->max_live);
-    if (a.blocks > kMaxBalBlocks) a.blocks = kMaxBalBlocks;
+    a.blocks = balance_blocks(plan->max_live, a.E, num_sms() < kMaxBalBlocks ? num_sms() : kMaxBalBlocks);
     a.balance_coef = balance_coef;
     a.z_coef = z_coef;
     a.counts = counts;
@@ -608,6 +739,7 @@ moe_status moe_balance_loss(const moe_plan* plan, const float* logits, const int
     const bool vec = a.E % 4 == 0 && ptr_aligned(logits, 16);
     cudaError_t e = by_width<LaunchStats>(a.E, vec, a, s);
     if (e != cudaSuccess) return MOE_ERR_CUDA;
+    if (a.blocks <= kClusterBlocks) return MOE_OK;
     const long long items = (long long)num_seqs * ((a.E + kFinCols - 1) / kFinCols);
     const long long cap = (long long)num_sms() * 2;
     e = launch_dependent(balance_finish_kernel, dim3((unsigned)(items < cap ? items : cap)), dim3(kFinThreads), 0, s,
@@ -637,7 +769,7 @@ moe_status moe_route_backward(const moe_plan* plan, const float* logits, const i
     a.E = plan->d.num_experts;
     a.k = plan->d.top_k;
     a.num_seqs = num_seqs;
-    a.blocks = balance_blocks(plan->max_live);
+    a.blocks = blocks_for(plan->max_live, kGradWarps * tokens_per_warp(a.E), (long long)num_sms() * 4);
     a.lse = lse;
     a.counts = counts;
     a.grad_scales = grad_scales;

@@ -19,67 +19,75 @@ namespace {
 
 constexpr int kI8Threads = 128;
 
-__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8]) {
-    f[0] = bf16lo(v.x); f[1] = bf16hi(v.x); f[2] = bf16lo(v.y); f[3] = bf16hi(v.y);
-    f[4] = bf16lo(v.z); f[5] = bf16hi(v.z); f[6] = bf16lo(v.w); f[7] = bf16hi(v.w);
-}
-// The largest magnitude of eight bf16 as bits: |v|'s bits order as its value, infinities and
-// NaN above every number.
-__device__ __forceinline__ uint32_t amax_bits(uint4 v, uint32_t a) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+// A row is taken by kWarps warps, which hold up to kHeld 16-byte chunks a lane: one read of the
+// row serves its largest magnitude and its codes.  Longer rows read the rest twice.
+constexpr int kHeld = 8;
+
+template <int kWarps>
+__device__ __forceinline__ uint32_t row_max(uint32_t a, uint32_t* s_red) {
+    a = __reduce_max_sync(0xffffffffu, a);
+    if (kWarps > 1) {
+        const int warp = threadIdx.x >> 5;
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) s_red[warp] = a;
+        __syncthreads();
+        const int w0 = warp / kWarps * kWarps;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        a = max(a, (w[i] << 16) & 0x7fffffffu);
-        a = max(a, w[i] & 0x7fff0000u);
+        for (int w = 0; w < kWarps; ++w) a = max(a, s_red[w0 + w]);
     }
     return a;
 }
-// fmaxf-like in bits: a NaN among them stays the largest, and int8_scale takes it for what it is.
-__device__ __forceinline__ float amax_of(uint32_t bits) { return __uint_as_float(bits); }
 
-__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
-    return (uint32_t)(a & 255) | ((uint32_t)(b & 255) << 8) | ((uint32_t)(c & 255) << 16) | ((uint32_t)d << 24);
-}
-__device__ __forceinline__ uint2 codes8(uint4 v, float scale) {
-    float f[8];
-    unpack8(v, f);
-    int q[8];
+// Quantises the row of `chunks` 16-byte chunks at src (none when !on): store(c, codes) for each
+// chunk; returns the scale.  Every thread of the row's warps calls it (with kWarps > 1, of the block).
+template <int kWarps, class Store>
+__device__ __forceinline__ float quantize_row(const uint4* src, int chunks, bool on, uint32_t* s_red, Store store) {
+    constexpr int kLanes = kWarps * 32;
+    const int lane = threadIdx.x & (kLanes - 1);
+    uint4 v[kHeld];
+    uint32_t a = 0u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q[i] = scale == scale ? int8_code(f[i], scale) : 0;
-    return make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+    for (int i = 0; i < kHeld; ++i) {
+        const int c = i * kLanes + lane;
+        v[i] = on && c < chunks ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) a = int8_amax_bits(v[i], a);
+    if (on)
+        for (int c = kHeld * kLanes + lane; c < chunks; c += kLanes) a = int8_amax_bits(__ldg(src + c), a);
+    const Int8Row row = int8_row(__uint_as_float(row_max<kWarps>(a, s_red)));
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int c = i * kLanes + lane;
+        if (on && c < chunks) store(c, int8_codes8(v[i], row));
+    }
+    if (on)
+        for (int c = kHeld * kLanes + lane; c < chunks; c += kLanes) store(c, int8_codes8(__ldg(src + c), row));
+    return row.scale;
 }
 
-__device__ __forceinline__ uint32_t block_max_u32(uint32_t a, uint32_t* s_red) {
-    a = __reduce_max_sync(0xffffffffu, a);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = a;
-    __syncthreads();
-    uint32_t m = 0u;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) m = max(m, s_red[w]);
-    return m;
-}
-
-// Rows of bf16: a block per row; one pass for the largest magnitude, one for the codes.
-__global__ void __launch_bounds__(kI8Threads) int8_quantize_rows_kernel(const uint4* __restrict__ in, long long rows,
+// Rows of bf16, kWarps warps a row.
+template <int kWarps>
+__global__ void __launch_bounds__(kI8Threads, 8) int8_quantize_rows_kernel(const uint4* __restrict__ in, long long rows,
                                                                         int chunks, long long ld_chunks,
                                                                         const int* __restrict__ live,
                                                                         uint2* __restrict__ q,
                                                                         float* __restrict__ scales) {
+    constexpr int kRows = kI8Threads / 32 / kWarps;  // rows a block holds
     __shared__ uint32_t s_red[kI8Threads / 32];
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();  // after the wait: a kernel released here may read what came before this one
     long long n = rows;
     if (live != nullptr) {
         const long long l = (long long)__ldg(live);
         n = l < 0 ? 0 : (l < rows ? l : rows);
     }
-    for (long long r = blockIdx.x; r < n; r += gridDim.x) {
-        const uint4* src = in + r * ld_chunks;
-        uint32_t a = 0u;
-        for (int c = threadIdx.x; c < chunks; c += kI8Threads) a = amax_bits(__ldg(src + c), a);
-        const float s = int8_scale(amax_of(block_max_u32(a, s_red)));
-        if (threadIdx.x == 0) scales[r] = s;
-        for (int c = threadIdx.x; c < chunks; c += kI8Threads) q[r * chunks + c] = codes8(__ldg(src + c), s);
+    for (long long r0 = (long long)blockIdx.x * kRows; r0 < n; r0 += (long long)gridDim.x * kRows) {
+        const long long r = r0 + threadIdx.x / (kWarps * 32);
+        const bool on = r < n;
+        const float s = quantize_row<kWarps>(in + r * ld_chunks, chunks, on, s_red,
+                                             [&](int c, uint2 codes) { q[r * chunks + c] = codes; });
+        if (on && (threadIdx.x & (kWarps * 32 - 1)) == 0) scales[r] = s;
     }
 }
 
@@ -100,42 +108,39 @@ __global__ void __launch_bounds__(kI8Threads) gather_rows_int8_kernel(const uint
     for (int t = blockIdx.x; t < n; t += gridDim.x) {
         __syncthreads();
         if (threadIdx.x < k) s_prow[threadIdx.x] = __ldg(inv + (size_t)t * k + threadIdx.x);
-        const uint4* src = x + (size_t)t * chunks;
-        uint32_t a = 0u;
-        for (int c = threadIdx.x; c < chunks; c += kI8Threads) a = amax_bits(__ldg(src + c), a);
-        const float s = int8_scale(amax_of(block_max_u32(a, s_red)));
-        if (threadIdx.x < k && s_prow[threadIdx.x] >= 0) xs[s_prow[threadIdx.x]] = s;
-        for (int c = threadIdx.x; c < chunks_out; c += kI8Threads) {
-            const uint2 codes = c < chunks ? codes8(__ldg(src + c), s) : make_uint2(0u, 0u);
+        // (the barriers of the row's maximum order s_prow before its readers)
+        auto put = [&](int c, uint2 codes) {
             for (int j = 0; j < k; ++j) {
                 const int pr = s_prow[j];
                 if (pr >= 0) xq[(size_t)pr * chunks_out + c] = codes;
             }
-        }
+        };
+        const float s = quantize_row<kI8Threads / 32>(x + (size_t)t * chunks, chunks, true, s_red, put);
+        if (threadIdx.x < k && s_prow[threadIdx.x] >= 0) xs[s_prow[threadIdx.x]] = s;
+        for (int c = chunks + threadIdx.x; c < chunks_out; c += kI8Threads) put(c, make_uint2(0u, 0u));
     }
 }
 
-// h rows: a block per live route quantises its bf16 row of the gate/up GEMM (pitch fp, zeros
+// h rows: kWarps warps per live route quantise its bf16 row of the gate/up GEMM (pitch fp, zeros
 // past F) with the row's own scale.
-__global__ void __launch_bounds__(kI8Threads) quantize_h_int8_kernel(const uint4* __restrict__ h,
+template <int kWarps>
+__global__ void __launch_bounds__(kI8Threads, 8) quantize_h_int8_kernel(const uint4* __restrict__ h,
                                                                      const int* __restrict__ live, int max_live,
                                                                      int k, int fp, const int* __restrict__ inv,
                                                                      uint2* __restrict__ hq, float* __restrict__ hs,
                                                                      const unsigned* status) {
+    constexpr int kRows = kI8Threads / 32 / kWarps;
     __shared__ uint32_t s_red[kI8Threads / 32];
     pdl_trigger();
     pdl_wait();
-    const int n = live_rows(live, max_live, status);
+    const long long n = (long long)live_rows(live, max_live, status) * k;
     const int chunks = fp / 8;
-    for (long long i = blockIdx.x; i < (long long)n * k; i += gridDim.x) {
-        const int pr = __ldg(inv + i);  // uniform over the block
-        if (pr < 0) continue;
-        const uint4* src = h + (size_t)pr * chunks;
-        uint32_t a = 0u;
-        for (int c = threadIdx.x; c < chunks; c += kI8Threads) a = amax_bits(__ldg(src + c), a);
-        const float s = int8_scale(amax_of(block_max_u32(a, s_red)));
-        if (threadIdx.x == 0) hs[pr] = s;
-        for (int c = threadIdx.x; c < chunks; c += kI8Threads) hq[(size_t)pr * chunks + c] = codes8(__ldg(src + c), s);
+    for (long long i0 = (long long)blockIdx.x * kRows; i0 < n; i0 += (long long)gridDim.x * kRows) {
+        const long long i = i0 + threadIdx.x / (kWarps * 32);
+        const int pr = i < n ? __ldg(inv + i) : -1;
+        const float s = quantize_row<kWarps>(h + (size_t)(pr < 0 ? 0 : pr) * chunks, chunks, pr >= 0, s_red,
+                                             [&](int c, uint2 codes) { hq[(size_t)pr * chunks + c] = codes; });
+        if (pr >= 0 && (threadIdx.x & (kWarps * 32 - 1)) == 0) hs[pr] = s;
     }
 }
 
@@ -166,14 +171,12 @@ __global__ void __launch_bounds__(kI8Threads) prepare_int8_kernel(
             src = wd + (size_t)r2 * (F / 8);
         }
         const int chunks = (first ? H : F) / 8, atoms = first ? at1 : at2, per = first ? w1r : hr;
-        uint32_t a = 0u;
-        for (int c = threadIdx.x; c < chunks; c += kI8Threads) a = amax_bits(__ldg(src + c), a);
-        const float s = int8_scale(amax_of(block_max_u32(a, s_red)));
         const long long grow = e * per + wrow;
-        if (threadIdx.x == 0) (first ? w1s : w2s)[grow] = s;
         uint2* dst = (first ? w1q : w2q) + ((size_t)(grow >> 7) * atoms * 128 + (grow & 127)) * 16;
-        for (int c = threadIdx.x; c < chunks; c += kI8Threads)
-            dst[(size_t)(c >> 4) * (128 * 16) + (c & 15)] = codes8(__ldg(src + c), s);
+        const float s = quantize_row<kI8Threads / 32>(src, chunks, true, s_red, [&](int c, uint2 codes) {
+            dst[(size_t)(c >> 4) * (128 * 16) + (c & 15)] = codes;
+        });
+        if (threadIdx.x == 0) (first ? w1s : w2s)[grow] = s;
     }
 }
 
@@ -240,11 +243,21 @@ size_t linear_scales_offset(long long rows, int cols_in) {
 
 }  // namespace
 
+// Whether `rows` rows of `chunks` 16-byte chunks are taken by a warp each: rows a warp can hold,
+// and enough of them to fill the SMs; else a block of four warps takes one.
+static bool warp_per_row(long long rows, int chunks) {
+    return chunks <= kHeld * 32 && rows >= (long long)num_sms() * 16;
+}
+
 cudaError_t launch_int8_quantize_rows(const __nv_bfloat16* in, long long rows, int cols, long long ld_in, int8_t* q,
                                       float* scales, const int* live, cudaStream_t s) {
-    return launch_dependent(int8_quantize_rows_kernel, dim3(capped_grid(rows, 16)), dim3(kI8Threads), 0, s,
-                            reinterpret_cast<const uint4*>(in), rows, cols / 8, ld_in / 8, live,
-                            reinterpret_cast<uint2*>(q), scales);
+    const uint4* src = reinterpret_cast<const uint4*>(in);
+    uint2* dst = reinterpret_cast<uint2*>(q);
+    if (warp_per_row(rows, cols / 8))
+        return launch_dependent(int8_quantize_rows_kernel<1>, dim3(capped_grid((rows + 3) / 4, 16)), dim3(kI8Threads), 0,
+                                s, src, rows, cols / 8, ld_in / 8, live, dst, scales);
+    return launch_dependent(int8_quantize_rows_kernel<4>, dim3(capped_grid(rows, 16)), dim3(kI8Threads), 0, s, src, rows,
+                            cols / 8, ld_in / 8, live, dst, scales);
 }
 
 cudaError_t launch_gather_int8(const __nv_bfloat16* x, const int* live, int max_live, int H, int hp, int k,
@@ -256,9 +269,14 @@ cudaError_t launch_gather_int8(const __nv_bfloat16* x, const int* live, int max_
 
 cudaError_t launch_quantize_h_int8(const __nv_bfloat16* h, const int* live, int max_live, int k, int fp,
                                    const int* inv, uint8_t* hq, float* hs, const unsigned* status, cudaStream_t s) {
-    return launch_dependent(quantize_h_int8_kernel, dim3(capped_grid((long long)max_live * k, 16)), dim3(kI8Threads),
-                            0, s, reinterpret_cast<const uint4*>(h), live, max_live, k, fp, inv,
-                            reinterpret_cast<uint2*>(hq), hs, status);
+    const long long rows = (long long)max_live * k;
+    const uint4* src = reinterpret_cast<const uint4*>(h);
+    uint2* dst = reinterpret_cast<uint2*>(hq);
+    if (warp_per_row(rows, fp / 8))
+        return launch_dependent(quantize_h_int8_kernel<1>, dim3(capped_grid((rows + 3) / 4, 16)), dim3(kI8Threads), 0, s,
+                                src, live, max_live, k, fp, inv, dst, hs, status);
+    return launch_dependent(quantize_h_int8_kernel<4>, dim3(capped_grid(rows, 16)), dim3(kI8Threads), 0, s, src, live,
+                            max_live, k, fp, inv, dst, hs, status);
 }
 
 cudaError_t launch_prepare_int8(const moe_plan* p, const __nv_bfloat16* wg, const __nv_bfloat16* wu,

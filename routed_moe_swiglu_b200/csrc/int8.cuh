@@ -23,8 +23,64 @@ __device__ __forceinline__ float int8_scale(float amax) {
     return amax > 0.0f ? __fdiv_rn(amax, 127.0f) : 1.0f;
 }
 __device__ __forceinline__ int int8_code(float v, float scale) {
-    const float q = __fdiv_rn(v, scale);  // NaN when the scale is: cvt gives 0
+    const float q = __fdiv_rn(v, scale);
     return __float2int_rn(fminf(fmaxf(q, -127.0f), 127.0f));
+}
+__device__ __forceinline__ uint32_t int8_pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+
+// A row's scale with what its codes are computed by.
+struct Int8Row {
+    float scale;
+    float inv;  // 1 / scale; 0 for a row of NaN, whose codes are 0; infinity: divide always
+};
+__device__ __forceinline__ Int8Row int8_row(float amax) {
+    Int8Row r;
+    r.scale = int8_scale(amax);
+    r.inv = r.scale == r.scale ? __frcp_rn(r.scale) : 0.0f;
+    if (r.scale < 1e-36f) r.inv = INFINITY;  // the reciprocal leaves the normal range
+    return r;
+}
+
+// Codes of eight bf16 (16 bytes) of a row.  The quotient's nearest whole number is taken from
+// v * inv, which is within 127 * 2^-23 = 1.6e-5 of the quotient rounded to fp32: both round to
+// the same number unless v * inv lies that near to a half, and then (and where the scale is
+// tiny) the eight are divided.  Half of the row's largest value is such a half in every row.
+__device__ __forceinline__ uint2 int8_codes8(uint4 v, const Int8Row& row) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t q[8];
+    // the farthest any v * inv lies from its whole number (a NaN or tiny scale: never near)
+    float off = row.inv > 0.0f && row.inv < INFINITY ? 0.0f : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float f = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+        // adding 1.5 * 2^23 leaves the nearest whole number (halves to even) in the low bits
+        const float t = fmaf(f, row.inv, 12582912.0f);
+        q[i] = __float_as_uint(t);
+        off = fmaxf(off, fabsf(fmaf(f, row.inv, 12582912.0f - t)));
+    }
+    if (!(off < 0.49998f)) {
+        if (row.inv == 0.0f) return make_uint2(0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float f = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+            q[i] = (uint32_t)int8_code(f, row.scale);
+        }
+    }
+    return make_uint2(int8_pack4(q[0], q[1], q[2], q[3]), int8_pack4(q[4], q[5], q[6], q[7]));
+}
+
+// The largest magnitude of eight bf16 and of a, as the bits of a non-negative fp32: these order
+// as their values, with infinity and then NaN above every number.
+__device__ __forceinline__ uint32_t int8_amax_bits(uint4 v, uint32_t a) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        a = max(a, (w[i] << 16) & 0x7fffffffu);
+        a = max(a, w[i] & 0x7fff0000u);
+    }
+    return a;
 }
 
 struct Int8Gemm {

@@ -144,8 +144,9 @@ def _check(r, ref, coef, zc, chosen=True):
     # the balance loss: positive terms, a product and a sum over E more than the sums
     assert abs(got[0] - ref["losses"][0]) <= (P_ERR + terms + 64) * U * ref["losses"][0]
     total = max(int(ref["n"].sum()), 1)
-    z_err = zc / total * (2 * np.abs(ref["lse"][al]) * lse_err + terms * U * ref["lse"][al] ** 2).sum()
-    assert abs(got[1] - ref["losses"][1]) <= z_err + 4 * U * abs(ref["losses"][1])
+    if zc:
+        z_err = zc / total * (2 * np.abs(ref["lse"][al]) * lse_err + terms * U * ref["lse"][al] ** 2).sum()
+        assert abs(got[1] - ref["losses"][1]) <= z_err + 4 * U * abs(ref["losses"][1])
     d = r.dlogits.cpu().double().numpy()
     assert (d[T:] == -5.0).all(), "rows past the live count were written"
     # each entry: P_ERR for p, <= 37 + 16 more in the two inner sums, a few products
@@ -219,6 +220,21 @@ def test_rows_that_nothing_is_left_of():
     r.backward()
     _check(r, _reference(q, 0.3, 0.1), 0.3, 0.1)
     assert r.losses.tolist() == [0.0, 0.0] and r.scales.tolist() == [0.0, 0.0, 0.0]
+
+
+def test_rows_near_the_bounds_of_the_type():
+    """Rows whose experts are all at the type's lowest value (equal shares), and rows far from zero
+    (the differences of their logits are exact, lse is not)."""
+    q = _problem(30, 24, 3, 1, seed=13)
+    q["logits"][3] = torch.finfo(torch.float32).min
+    q["logits"][4] = torch.finfo(torch.float32).min
+    q["logits"][4, 7] = torch.finfo(torch.float32).max
+    q["logits"][8] = torch.round(q["logits"][8] * 1024) / 1024 + 8192
+    q["logits"][9] = torch.round(q["logits"][9] * 1024) / 1024 - 8192
+    r = _Run(q)
+    r.forward(0.3, 0.0)
+    r.backward()
+    _check(r, _reference(q, 0.3, 0.0), 0.3, 0.0)
 
 
 def test_nan_in_a_counted_row_shows():
