@@ -32,7 +32,7 @@
 namespace moe {
 namespace {
 
-constexpr int kStagesMax = 5;
+constexpr int kStagesMax = 6;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr int kPairM = 256;
@@ -42,11 +42,13 @@ constexpr uint32_t kABytes = kAtoms * kAtomBytes;    // 32 KB: this CTA's 128 we
 constexpr uint32_t kBBytesMax = kAtoms * kAtomBytes; // up to 128 activation rows per CTA
 constexpr uint32_t kAccCols = 256;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kStageRegion = 4 * (kABytes + 16384);  // also 3 * (32 + 32) and 5 * (32 + 6) KB
-constexpr uint32_t kEpiBox = 32 * 32 * 4 + 128;           // transpose box and 32 row scales of a warp
-constexpr size_t kSmemBytes = 1024 + kStageRegion + kEpiWarps * kEpiBox + 256;
+constexpr uint32_t kStageRegion = 6 * (kABytes + 4096);  // also 5 * (32 + 8), 4 * (32 + 16) and 3 * (32 + 32) KB
+constexpr int kWarpCols = 128;                            // activation rows of a tile that an epilogue warp drains
+constexpr uint32_t kEpiBytes = kWarpCols * 2 * 4;         // their scales and, gate/up, probabilities
+constexpr size_t kSmemBytes = 1024 + kStageRegion + kEpiWarps * kEpiBytes + 256;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
-static_assert(kStageRegion >= 3 * (kABytes + kBBytesMax), "three full-width stages");
+static_assert(kStageRegion >= 3 * (kABytes + kBBytesMax) && kStageRegion >= 4 * (kABytes + 16384) &&
+                  kStageRegion >= 5 * (kABytes + 8192), "stages");
 
 struct __align__(8) Barriers {
     uint64_t full[kStagesMax];   // CTA 0's counts both CTAs' loads of a stage
@@ -80,21 +82,12 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const CUtensorMap* m
         : "memory");
 }
 
-__device__ __forceinline__ float silu_f(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 // x clamped to [-c, c]; a NaN (a row that holds one) stays NaN.
 __device__ __forceinline__ float clamp_nan(float x, float c) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;\n\tmin.NaN.f32 %0, %0, %3;" : "=f"(r) : "f"(x), "f"(-c), "f"(c));
     return r;
 }
-__device__ __forceinline__ float swiglu_value(float g, float u, float clamp) {
-    if (clamp > 0.0f) {
-        g = clamp_nan(g, clamp);
-        u = clamp_nan(u, clamp);
-    }
-    return silu_f(g) * u;
-}
-
 __device__ __forceinline__ int tile_n(int nvalid) { return (nvalid + 31) & ~31; }
 
 struct StageCfg {
@@ -103,7 +96,8 @@ struct StageCfg {
 };
 __device__ __forceinline__ StageCfg stage_cfg(int widest_tile) {
     const int hb = tile_n(widest_tile) >> 1;  // activation rows per CTA
-    if (hb <= 16) return {5, 4096u};
+    if (hb <= 16) return {6, 4096u};
+    if (hb <= 32) return {5, 8192u};
     if (hb <= 64) return {4, 16384u};
     return {3, kBBytesMax};
 }
@@ -118,14 +112,10 @@ __device__ __forceinline__ int4 tile_of(const Int8Gemm& p, int mt, int rows) {
     return make_int4(0, m0, min(kRouteTile, rows - m0), m0);
 }
 
-// Four outputs of one row, from int32 sums.
-__device__ __forceinline__ float4 scaled4(int4 v, float xs, float4 ws) {
-    return make_float4(__int2float_rn(v.x) * xs * ws.x, __int2float_rn(v.y) * xs * ws.y,
-                       __int2float_rn(v.z) * xs * ws.z, __int2float_rn(v.w) * xs * ws.w);
-}
-__device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&v);
+// Arrive on an mbarrier of the cluster without ordering this thread's stores before it: what the
+// arrival says is that the accumulator's loads are done, which tcgen05.wait::ld has waited for.
+__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 template <int kMode>
@@ -134,7 +124,7 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sEpi = smem + kStageRegion;
-    Barriers* bars = reinterpret_cast<Barriers*>(sEpi + kEpiWarps * kEpiBox);
+    Barriers* bars = reinterpret_cast<Barriers*>(sEpi + kEpiWarps * kEpiBytes);
     volatile int* abort_flag = &bars->abort_flag;
 
     const int warp = threadIdx.x >> 5;
@@ -301,22 +291,53 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
         }
         __syncwarp();
     } else {
-        // ---------------- epilogue: warps 2..9
+        // ---------------- epilogue: warps 2..9.  TMEM lanes are weight rows (output columns),
+        // TMEM columns activation rows: a lane's weight scale is a register, a row's scale comes from
+        // shared memory, and the 32 lanes' stores of one row are neighbours.  The next tile's scales
+        // are fetched while this one is drained.
         const int ew = warp - 2;
         const int quad = warp & 3;  // TMEM lane quarter this warp may read
         const int half = ew >> 2;   // this warp takes the 32-row chunks c with c % 2 == half
         const uint32_t acc_empty0[2] = {map_to_cta(smem_u32(&bars->acc_empty[0]), 0),
                                         map_to_cta(smem_u32(&bars->acc_empty[1]), 0)};
-        uint8_t* tbuf = sEpi + (size_t)ew * kEpiBox;
-        float* s_xs = reinterpret_cast<float*>(tbuf + 32 * 32 * 4);
+        float* s_xs = reinterpret_cast<float*>(sEpi + (size_t)ew * kEpiBytes);
+        float* s_pr = s_xs + kWarpCols;
+        const bool has_pr = kMode == kGateUp && p.route_probs != nullptr;
+        int4 ti_next = make_int4(0, 0, 0, 0);
+        float xs_next[4], pr_next[4], ws_next = 0.0f;
+        auto first_row = [&](int t) {  // this warp's first weight row in tile t
+            return (t % p.n_tiles) * kPairM + 128 * (int)rank + 32 * quad;
+        };
+        auto fetch = [&](int t) {
+            if (t >= total_tiles) return;
+            ti_next = tile_of<kMode>(p, t / p.n_tiles, rows);
+            const int w = first_row(t) + lane;
+            if (kMode == kGateUp || w < p.out_cols)
+                ws_next = __ldg(p.w_scale + (kMode == kDense ? 0 : (size_t)ti_next.x * p.a_rows) + w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = (half + 2 * i) * 32 + lane;
+                xs_next[i] = r < ti_next.z ? __ldg(p.row_scale + ti_next.y + r) : 0.0f;
+                if (has_pr) pr_next[i] = r < ti_next.z ? __ldg(p.route_probs + __ldg(p.perm + ti_next.w + r)) : 0.0f;
+            }
+        };
+        fetch(pair);
         int it = 0;
         for (int t = pair; t < total_tiles; t += npairs, ++it) {
             const int buf = it & 1;
             const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
-            const int mt = t / p.n_tiles, nt = t - mt * p.n_tiles;
-            const int4 ti = tile_of<kMode>(p, mt, rows);
+            const int4 ti = ti_next;
+            const float ws = ws_next;
             const int nch = tile_n(ti.z) >> 5;
-            const int w0 = nt * kPairM + 128 * (int)rank + 32 * quad;  // this warp's first weight row
+            const int w0 = first_row(t);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                s_xs[i * 32 + lane] = xs_next[i];
+                if (has_pr) s_pr[i * 32 + lane] = pr_next[i];
+            }
+            __syncwarp();
+            fetch(t + npairs);
             const bool got = __all_sync(0xffffffffu,
                                         mbar_wait_bounded(&bars->acc_full[buf], acc_phase, abort_flag, p.wait_limit_ns));
             if (!got) {
@@ -325,148 +346,79 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
             }
             tc_fence_after_sync();
             const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)buf * kAccCols;
-            if (kMode == kGateUp) {
-                // lanes are weight rows: their scale in a register, the 32 activation rows' in shared memory
-                const float ws = __ldg(p.w_scale + (size_t)ti.x * p.a_rows + w0 + lane);
-                __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(p.out);
-                const bool lo = lane < 16;
-                const int f0 = p.relu2 ? w0 : w0 >> 1;  // first of this warp's 32 (16) f
-                if (f0 < p.out_cols) {
+            const int f0 = p.relu2 ? w0 : w0 >> 1;  // gate/up: first of this warp's 32 (16) f
+            const bool cols = (kMode == kGateUp ? f0 : w0) < p.out_cols;
 #pragma unroll 1
-                    for (int c = half; c < nch; c += 2) {
-                        uint32_t v[32];
-                        tmem_ld_32x32b_x32(taddr + c * 32, v);
-                        const bool row_ok = c * 32 + lane < ti.z;
-                        s_xs[lane] = row_ok ? __ldg(p.row_scale + ti.y + c * 32 + lane) : 0.0f;
-                        float pv = 1.0f;
-                        if (p.route_probs != nullptr && row_ok)
-                            pv = __ldg(p.route_probs + __ldg(p.perm + ti.w + c * 32 + lane));
-                        tmem_ld_wait();
-                        __syncwarp();
-                        float g[32];
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) g[j] = __int2float_rn((int)v[j]) * s_xs[j] * ws;
-                        if (p.relu2) {
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) {
-                                float x = g[j];
-                                if (p.clamp > 0.0f) x = clamp_nan(x, p.clamp);
-                                const float r = x > 0.0f || x != x ? x : 0.0f;  // a NaN row stays NaN
-                                float hv = r * r;
-                                if (p.route_probs != nullptr) hv *= __shfl_sync(0xffffffffu, pv, j);
-                                *reinterpret_cast<__nv_bfloat16*>(tbuf + j * 64 + lane * 2) = __float2bfloat16_rn(hv);
-                            }
-                            __syncwarp();
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int r = i * 8 + (lane >> 2);
-                                const int route = c * 32 + r;
-                                const uint4 w = *reinterpret_cast<const uint4*>(tbuf + r * 64 + (lane & 3) * 16);
-                                if (route < ti.z && f0 + (lane & 3) * 8 < p.out_cols)
-                                    *reinterpret_cast<uint4*>(h + (size_t)(ti.y + route) * (size_t)p.out_ld + f0 +
-                                                              (lane & 3) * 8) = w;
-                            }
-                        } else {
-                            // lanes < 16 keep the gate values of routes 0..15 and receive the up values;
-                            // lanes >= 16 keep the up values of routes 16..31 and receive the gate values
-                            uint8_t* row0 = tbuf + (lo ? 0 : 16 * 32 + 64) + (lane & 15) * 2;
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float mine = lo ? g[j] : g[16 + j];
-                                const float other = __shfl_xor_sync(0xffffffffu, lo ? g[16 + j] : g[j], 16);
-                                float hv = swiglu_value(lo ? mine : other, lo ? other : mine, p.clamp);
-                                if (p.route_probs != nullptr) hv *= __shfl_sync(0xffffffffu, pv, lo ? j : 16 + j);
-                                *reinterpret_cast<__nv_bfloat16*>(row0 + j * 32) = __float2bfloat16_rn(hv);
-                            }
-                            __syncwarp();
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const int r = i * 16 + (lane >> 1);
-                                const int route = c * 32 + r;
-                                const uint4 w = *reinterpret_cast<const uint4*>(tbuf + r * 32 + (r >= 16 ? 64 : 0) +
-                                                                                (lane & 1) * 16);
-                                if (route < ti.z)
-                                    *reinterpret_cast<uint4*>(h + (size_t)(ti.y + route) * (size_t)p.out_ld + f0 +
-                                                              (lane & 1) * 8) = w;
-                            }
-                        }
-                        __syncwarp();
-                    }
-                }
-            } else if (w0 < p.out_cols) {
-                // transpose the int32 sums; a lane then holds 8 (bf16) or 4 (fp32) columns of a row
-                const bool bf16 = kMode == kDense && p.out_bf16 != 0;
-                const int cl = bf16 ? (lane & 3) * 8 : (lane & 7) * 4;  // the lane's first column of 32
-                const float* wsp = p.w_scale + (kMode == kDense ? 0 : (size_t)ti.x * p.a_rows) + w0 + cl;
-                float wsr[8];
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    wsr[q] = (q < 4 || bf16) && w0 + cl + q < p.out_cols ? __ldg(wsp + q) : 0.0f;
-                const float4 ws0 = make_float4(wsr[0], wsr[1], wsr[2], wsr[3]);
-                const float4 ws1 = make_float4(wsr[4], wsr[5], wsr[6], wsr[7]);
-                // whole 16-byte stores: every lane column group inside out, rows 16-byte aligned
-                const bool wide = kMode == kDown ||
-                                  (p.out_ld % (bf16 ? 8 : 4) == 0 && (reinterpret_cast<uintptr_t>(p.out) & 15) == 0);
-                const int valid = p.out_cols - w0 - cl;  // columns of this lane inside out (may be <= 0 or > 8)
-#pragma unroll 1
-                for (int c = half; c < nch; c += 2) {
-                    uint32_t v[32];
-                    tmem_ld_32x32b_x32(taddr + c * 32, v);
-                    s_xs[lane] = c * 32 + lane < ti.z ? __ldg(p.row_scale + ti.y + c * 32 + lane) : 0.0f;
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int r = 0; r < 32; ++r) *reinterpret_cast<uint32_t*>(tbuf + r * 128 + lane * 4) = v[r];
+            for (int c = half; c < nch; c += 2) {
+                uint32_t v[32];
+                tmem_ld_32x32b_x32(taddr + c * 32, v);
+                tmem_ld_wait();
+                if (c + 2 >= nch) {  // the last of this warp's columns is in registers
+                    tc_fence_before_sync();
                     __syncwarp();
-                    if (bf16) {
-                        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.out);
+                    if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty0[buf]);
+                }
+                if (!cols) continue;
+                const float4* xs4 = reinterpret_cast<const float4*>(s_xs + (c >> 1) * 32);
+                float g[32];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int r = i * 8 + (lane >> 2);
-                            const int row = c * 32 + r;
-                            const int4 v0 = *reinterpret_cast<const int4*>(tbuf + r * 128 + cl * 4);
-                            const int4 v1 = *reinterpret_cast<const int4*>(tbuf + r * 128 + cl * 4 + 16);
-                            const float xs = s_xs[r];
-                            const float4 a = scaled4(v0, xs, ws0), b = scaled4(v1, xs, ws1);
-                            const uint4 w = make_uint4(bf16x2(a.x, a.y), bf16x2(a.z, a.w), bf16x2(b.x, b.y),
-                                                       bf16x2(b.z, b.w));
-                            if (row >= ti.z) continue;
-                            __nv_bfloat16* dst = out + (size_t)(ti.y + row) * (size_t)p.out_ld + w0 + cl;
-                            if (wide && valid >= 8) {
-                                *reinterpret_cast<uint4*>(dst) = w;
-                            } else {
-                                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+                for (int q = 0; q < 8; ++q) {
+                    const float4 xs = xs4[q];
+                    g[4 * q] = __int2float_rn((int)v[4 * q]) * xs.x * ws;
+                    g[4 * q + 1] = __int2float_rn((int)v[4 * q + 1]) * xs.y * ws;
+                    g[4 * q + 2] = __int2float_rn((int)v[4 * q + 2]) * xs.z * ws;
+                    g[4 * q + 3] = __int2float_rn((int)v[4 * q + 3]) * xs.w * ws;
+                }
+                const int left = ti.z - c * 32;  // rows of this chunk that exist (may be more than 32)
+                if (kMode == kGateUp) {
+                    __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(p.out) +
+                                       (size_t)(ti.y + c * 32) * (size_t)p.out_ld + f0;
+                    const float* pr = s_pr + (c >> 1) * 32;
+                    if (p.clamp > 0.0f) {
 #pragma unroll
-                                for (int q = 0; q < 8; ++q)
-                                    if (q < valid)
-                                        reinterpret_cast<uint16_t*>(dst)[q] = (uint16_t)(ww[q >> 1] >> (16 * (q & 1)));
-                            }
+                        for (int j = 0; j < 32; ++j) g[j] = clamp_nan(g[j], p.clamp);
+                    }
+                    if (p.relu2) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const float r = g[j] > 0.0f || g[j] != g[j] ? g[j] : 0.0f;  // a NaN row stays NaN
+                            float hv = r * r;
+                            if (has_pr) hv *= pr[j];
+                            if (j < left) h[(size_t)j * (size_t)p.out_ld + lane] = __float2bfloat16_rn(hv);
                         }
                     } else {
-                        float* out = reinterpret_cast<float*>(p.out);
+                        // lanes < 16 hold gate, the others up of the same f: lanes < 16 keep rows 0..15
+                        // and receive their up values, the others keep rows 16..31 and receive gate.
+                        // silu(g) * u = g * u / (1 + exp(-g)), and the product does not ask which is which
+                        const bool lo = lane < 16;
+                        const int r0 = lo ? 0 : 16;
+                        __nv_bfloat16* dst = h + (size_t)r0 * (size_t)p.out_ld + (lane & 15);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = i * 4 + (lane >> 3);
-                            const int row = c * 32 + r;
-                            const float4 a = scaled4(*reinterpret_cast<const int4*>(tbuf + r * 128 + cl * 4), s_xs[r],
-                                                     ws0);
-                            if (row >= ti.z) continue;
-                            float* dst = out + (size_t)(ti.y + row) * (size_t)p.out_ld + w0 + cl;
-                            if (wide && valid >= 4) {
-                                *reinterpret_cast<float4*>(dst) = a;
-                            } else {
-                                const float aa[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)
-                                    if (q < valid) dst[q] = aa[q];
-                            }
+                        for (int j = 0; j < 16; ++j) {
+                            const float mine = lo ? g[j] : g[16 + j];
+                            const float other = __shfl_xor_sync(0xffffffffu, lo ? g[16 + j] : g[j], 16);
+                            const float gate = lo ? mine : other;
+                            float hv = __fdividef(mine * other, 1.0f + __expf(-gate));
+                            if (has_pr) hv *= pr[r0 + j];
+                            if (r0 + j < left) dst[(size_t)j * (size_t)p.out_ld] = __float2bfloat16_rn(hv);
                         }
                     }
-                    __syncwarp();
+                } else if (w0 + lane < p.out_cols) {
+                    const size_t at = (size_t)(ti.y + c * 32) * (size_t)p.out_ld + w0 + lane;
+                    if (kMode == kDense && p.out_bf16 != 0) {
+                        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < left) dst[(size_t)j * (size_t)p.out_ld] = __float2bfloat16_rn(g[j]);
+                    } else {
+                        float* dst = reinterpret_cast<float*>(p.out) + at;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j < left) dst[(size_t)j * (size_t)p.out_ld] = g[j];
+                    }
                 }
             }
-            tc_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acc_empty0[buf]);  // release on CTA 0's barrier
+            if (nch <= half && lane == 0) mbar_arrive_cluster_relaxed(acc_empty0[buf]);  // no column of this warp
         }
     }
 

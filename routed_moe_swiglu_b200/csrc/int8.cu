@@ -52,10 +52,10 @@ __device__ __forceinline__ float quantize_row(const uint4* src, int chunks, bool
         v[i] = on && c < chunks ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
     }
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) a = int8_amax_bits(v[i], a);
+    for (int i = 0; i < kHeld; ++i) a = int8_amax_pairs(v[i], a);
     if (on)
-        for (int c = kHeld * kLanes + lane; c < chunks; c += kLanes) a = int8_amax_bits(__ldg(src + c), a);
-    const Int8Row row = int8_row(__uint_as_float(row_max<kWarps>(a, s_red)));
+        for (int c = kHeld * kLanes + lane; c < chunks; c += kLanes) a = int8_amax_pairs(__ldg(src + c), a);
+    const Int8Row row = int8_row(__uint_as_float(row_max<kWarps>(int8_amax_bits(a), s_red)));
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
         const int c = i * kLanes + lane;
@@ -68,7 +68,7 @@ __device__ __forceinline__ float quantize_row(const uint4* src, int chunks, bool
 
 // Rows of bf16, kWarps warps a row.
 template <int kWarps>
-__global__ void __launch_bounds__(kI8Threads, 8) int8_quantize_rows_kernel(const uint4* __restrict__ in, long long rows,
+__global__ void __launch_bounds__(kI8Threads, 6) int8_quantize_rows_kernel(const uint4* __restrict__ in, long long rows,
                                                                         int chunks, long long ld_chunks,
                                                                         const int* __restrict__ live,
                                                                         uint2* __restrict__ q,
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kI8Threads) gather_rows_int8_kernel(const uint
 // h rows: kWarps warps per live route quantise its bf16 row of the gate/up GEMM (pitch fp, zeros
 // past F) with the row's own scale.
 template <int kWarps>
-__global__ void __launch_bounds__(kI8Threads, 8) quantize_h_int8_kernel(const uint4* __restrict__ h,
+__global__ void __launch_bounds__(kI8Threads, 6) quantize_h_int8_kernel(const uint4* __restrict__ h,
                                                                      const int* __restrict__ live, int max_live,
                                                                      int k, int fp, const int* __restrict__ inv,
                                                                      uint2* __restrict__ hq, float* __restrict__ hs,

@@ -31,57 +31,65 @@ __device__ __forceinline__ uint32_t int8_pack4(uint32_t a, uint32_t b, uint32_t 
 }
 
 // A row's scale with what its codes are computed by.
+//
+// Codes without a division.  With amax = A 2^a and |value| = X 2^b (A, X whole numbers below
+// 256: bf16), value / scale is 127 X 2^e / A but for the roundings of the scale and of the
+// quotient, e = b - a <= 0.  Either that ratio is a half (m + 1/2) or it lies at least
+// 2^e / (2 A) > 2^e / 512 from every half, while the roundings move it by less than
+// 254 * 2^e * 2^-23 < 2^e / 2^15: away from halves, value * inv with any inv within 2^-20 of
+// 1 / scale gives the code.  A half needs 254 X 2^e = (2m + 1) A.  As 127 is a prime and
+// 2m + 1 <= 254, either 127 divides A (A = 254: the scale is a power of two, 1 / scale and every
+// product are exact, and halves go to even as they do in the division) or 2m + 1 = 127: the
+// value is half of the largest.  Its quotient is one number for the whole row; inv is moved by
+// 2^-21 of itself so that value * inv falls to the side of 63.5 that this quotient is rounded to.
 struct Int8Row {
     float scale;
-    float inv;  // 1 / scale; 0 for a row of NaN, whose codes are 0; infinity: divide always
+    float inv;
+    bool divide;  // a subnormal scale (its rounding is coarser), or a row of NaN: see int8_codes8
 };
 __device__ __forceinline__ Int8Row int8_row(float amax) {
     Int8Row r;
     r.scale = int8_scale(amax);
-    r.inv = r.scale == r.scale ? __frcp_rn(r.scale) : 0.0f;
-    if (r.scale < 1e-36f) r.inv = INFINITY;  // the reciprocal leaves the normal range
+    r.divide = !(r.scale >= 1.1754943508222875e-38f);
+    r.inv = __frcp_rn(r.scale);
+    if ((__float_as_uint(amax) & 0x007f0000u) != 0x007e0000u) {  // A != 254
+        const float half = __fdiv_rn(0.5f * amax, r.scale);
+        r.inv *= __float2int_rn(half) == 64 ? 1.0f + 0x1p-21f : 1.0f - 0x1p-21f;
+    }
     return r;
 }
 
-// Codes of eight bf16 (16 bytes) of a row.  The quotient's nearest whole number is taken from
-// v * inv, which is within 127 * 2^-23 = 1.6e-5 of the quotient rounded to fp32: both round to
-// the same number unless v * inv lies that near to a half, and then (and where the scale is
-// tiny) the eight are divided.  Half of the row's largest value is such a half in every row.
+// Codes of eight bf16 (16 bytes) of a row.
 __device__ __forceinline__ uint2 int8_codes8(uint4 v, const Int8Row& row) {
     const uint32_t w[4] = {v.x, v.y, v.z, v.w};
     uint32_t q[8];
-    // the farthest any v * inv lies from its whole number (a NaN or tiny scale: never near)
-    float off = row.inv > 0.0f && row.inv < INFINITY ? 0.0f : 1.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float f = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-        // adding 1.5 * 2^23 leaves the nearest whole number (halves to even) in the low bits
-        const float t = fmaf(f, row.inv, 12582912.0f);
-        q[i] = __float_as_uint(t);
-        off = fmaxf(off, fabsf(fmaf(f, row.inv, 12582912.0f - t)));
-    }
-    if (!(off < 0.49998f)) {
-        if (row.inv == 0.0f) return make_uint2(0u, 0u);
+    if (!row.divide) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float f = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
-            q[i] = (uint32_t)int8_code(f, row.scale);
+            // adding 1.5 * 2^23 leaves the nearest whole number (halves to even) in the low bits
+            q[i] = __float_as_uint(fmaf(f, row.inv, 12582912.0f));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float f = __uint_as_float(i & 1 ? w[i >> 1] & 0xffff0000u : w[i >> 1] << 16);
+            q[i] = row.scale == row.scale ? (uint32_t)int8_code(f, row.scale) : 0u;
         }
     }
     return make_uint2(int8_pack4(q[0], q[1], q[2], q[3]), int8_pack4(q[4], q[5], q[6], q[7]));
 }
 
-// The largest magnitude of eight bf16 and of a, as the bits of a non-negative fp32: these order
-// as their values, with infinity and then NaN above every number.
-__device__ __forceinline__ uint32_t int8_amax_bits(uint4 v, uint32_t a) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        a = max(a, (w[i] << 16) & 0x7fffffffu);
-        a = max(a, w[i] & 0x7fff0000u);
-    }
-    return a;
+// The largest magnitudes of bf16 pairs, as their 15 bits: these order as the values, with
+// infinity and then NaN above every number.
+__device__ __forceinline__ uint32_t int8_amax_pairs(uint4 v, uint32_t a) {
+    a = __vmaxu2(a, v.x & 0x7fff7fffu);
+    a = __vmaxu2(a, v.y & 0x7fff7fffu);
+    a = __vmaxu2(a, v.z & 0x7fff7fffu);
+    return __vmaxu2(a, v.w & 0x7fff7fffu);
 }
+// The larger of a pair, as the bits of an fp32.
+__device__ __forceinline__ uint32_t int8_amax_bits(uint32_t a) { return max(a << 16, a & 0xffff0000u); }
 
 struct Int8Gemm {
     const int4* tiles;              // grouped: {expert, first padded row, valid rows, first permuted row}
