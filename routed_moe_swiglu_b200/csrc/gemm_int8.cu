@@ -22,8 +22,8 @@
 // side; what stands there on the weight side is then of no account (integers
 // have no NaN).
 //
-// Roles (10 warps per CTA): warp 0 issues TMA loads; warp 1 owns TMEM and, in
-// CTA 0, issues the MMAs; warps 2-9 drain two accumulators of 256 columns.
+// Roles (18 warps per CTA): warp 0 issues TMA loads; warp 1 owns TMEM and, in
+// CTA 0, issues the MMAs; warps 2-17 drain two accumulators of 256 columns.
 // Every mbarrier wait is bounded; the pair meets in cluster barriers only at
 // start-up and before TMEM is released.
 #include "int8.cuh"
@@ -33,8 +33,10 @@ namespace moe {
 namespace {
 
 constexpr int kStagesMax = 6;
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = (2 + kEpiWarps) * 32;
+constexpr int kEpiWarps = 8;    // of a group: each drains a quarter of the lanes and half of the columns
+constexpr int kEpiGroups = 2;   // groups of epilogue warps, which take tiles in turn
+constexpr int kThreads = (2 + kEpiGroups * kEpiWarps) * 32;
+constexpr int kChunk = 16;      // accumulator columns a warp takes at once
 constexpr int kPairM = 256;
 constexpr int kAtoms = 2;                            // 128-byte swizzle atoms per stage
 constexpr uint32_t kAtomBytes = 128 * 128;           // 128 rows of 128 bytes
@@ -44,8 +46,8 @@ constexpr uint32_t kAccCols = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kStageRegion = 6 * (kABytes + 4096);  // also 5 * (32 + 8), 4 * (32 + 16) and 3 * (32 + 32) KB
 constexpr int kWarpCols = 128;                            // activation rows of a tile that an epilogue warp drains
-constexpr uint32_t kEpiBytes = kWarpCols * 2 * 4;         // their scales and, gate/up, probabilities
-constexpr size_t kSmemBytes = 1024 + kStageRegion + kEpiWarps * kEpiBytes + 256;
+constexpr uint32_t kEpiBytes = kWarpCols * 4;             // their scales
+constexpr size_t kSmemBytes = 1024 + kStageRegion + kEpiGroups * kEpiWarps * kEpiBytes + 256;
 static_assert(kSmemBytes <= 232448, "shared memory budget");
 static_assert(kStageRegion >= 3 * (kABytes + kBBytesMax) && kStageRegion >= 4 * (kABytes + 16384) &&
                   kStageRegion >= 5 * (kABytes + 8192), "stages");
@@ -112,6 +114,38 @@ __device__ __forceinline__ int4 tile_of(const Int8Gemm& p, int mt, int rows) {
     return make_int4(0, m0, min(kRouteTile, rows - m0), m0);
 }
 
+// Each thread of the warp reads 16 consecutive 32-bit columns of its TMEM lane.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+// 1 / (1 + exp(-g)) from the approximate exponential and reciprocal (2^-22 and 1 ulp; the
+// exponent's rounding adds |g| 2^-24): far below the bf16 step that h is rounded to.
+__device__ __forceinline__ float sigmoid_approx(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+__device__ __forceinline__ void store_as(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_as(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+// The lane's values of n rows, ld apart; of the first `left` of them only.
+template <int n, class T>
+__device__ __forceinline__ void store_rows(T* dst, long long ld, const float (&v)[n], int left) {
+    if (left >= n) {
+#pragma unroll
+        for (int j = 0; j < n; ++j) store_as(dst + (size_t)j * (size_t)ld, v[j]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < n; ++j)
+            if (j < left) store_as(dst + (size_t)j * (size_t)ld, v[j]);
+    }
+}
 // Arrive on an mbarrier of the cluster without ordering this thread's stores before it: what the
 // arrival says is that the accumulator's loads are done, which tcgen05.wait::ld has waited for.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
@@ -124,7 +158,7 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sEpi = smem + kStageRegion;
-    Barriers* bars = reinterpret_cast<Barriers*>(sEpi + kEpiWarps * kEpiBytes);
+    Barriers* bars = reinterpret_cast<Barriers*>(sEpi + kEpiGroups * kEpiWarps * kEpiBytes);
     volatile int* abort_flag = &bars->abort_flag;
 
     const int warp = threadIdx.x >> 5;
@@ -188,9 +222,11 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
             bool ok = true;
             int last_phase[kStagesMax];
             for (int s = 0; s < kStagesMax; ++s) last_phase[s] = -1;
+            int4 ti_n = total_tiles > pair ? tile_of<kMode>(p, pair / p.n_tiles, rows) : make_int4(0,0,0,0);
             for (int t = pair; t < total_tiles && ok; t += npairs) {
                 const int mt = t / p.n_tiles, nt = t - mt * p.n_tiles;
-                const int4 ti = tile_of<kMode>(p, mt, rows);
+                const int4 ti = ti_n;
+                if (t + npairs < total_tiles) ti_n = tile_of<kMode>(p, (t + npairs) / p.n_tiles, rows);
                 const int hb = tile_n(ti.z) >> 1;
                 const uint32_t tx = 2u * (kABytes + (uint32_t)hb * (kAtoms * 128u));
                 const CUtensorMap* mb = &tmB->m[(hb >> 4) - 1];
@@ -244,16 +280,19 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
     } else if (warp == 1) {
         if (lane == 0 && leader) {
             // ---------------- pair MMA issuer (CTA 0)
+            const uint64_t a_desc0 = sdesc_kmajor_sw128(smem_u32(sA)), b_desc0 = sdesc_kmajor_sw128(smem_u32(sB));
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
             int it = 0;
+            int zn = total_tiles > pair ? tile_of<kMode>(p, pair / p.n_tiles, rows).z : 0;
             for (int t = pair; t < total_tiles && ok; t += npairs, ++it) {
                 const int buf = it & 1;
                 const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
-                const int n = tile_n(tile_of<kMode>(p, t / p.n_tiles, rows).z);
+                const int n = tile_n(zn);
+                if (t + npairs < total_tiles) zn = tile_of<kMode>(p, (t + npairs) / p.n_tiles, rows).z;
                 const uint32_t idesc = idesc_i8(kPairM, n);
-                const uint32_t b_atom = (uint32_t)(n >> 1) * 128u;  // bytes of one atom of this CTA's rows
+                const uint32_t b_atom16 = (uint32_t)(n >> 1) * 8u;  // one atom of this CTA's rows, in 16 bytes
                 if (!mbar_wait_bounded(&bars->acc_empty[buf], acc_phase ^ 1u, abort_flag, p.wait_limit_ns)) {
                     ok = false;
                     break;
@@ -266,15 +305,15 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
                         break;
                     }
                     tc_fence_after_sync();
-                    const uint32_t a_addr = smem_u32(sA + stage * kABytes);
-                    const uint32_t b_addr = smem_u32(sB + stage * kBBytes);
+                    // operand addresses are descriptor fields in units of 16 bytes: a stage's, an
+                    // atom's and a step's offsets are added to the first stage's descriptors
+                    const uint64_t da = a_desc0 + (uint64_t)((uint32_t)stage * (kABytes >> 4));
+                    const uint64_t db = b_desc0 + (uint64_t)((uint32_t)stage * (kBBytes >> 4));
 #pragma unroll
-                    for (int kk = 0; kk < kAtoms * 4; ++kk) {  // 32 elements of K each
-                        const uint32_t koff = (uint32_t)(kk & 3) * 32;
-                        mma_i8_pair(d_tmem, sdesc_kmajor_sw128(a_addr + (uint32_t)(kk >> 2) * kAtomBytes + koff),
-                                    sdesc_kmajor_sw128(b_addr + (uint32_t)(kk >> 2) * b_atom + koff), idesc,
+                    for (int kk = 0; kk < kAtoms * 4; ++kk)  // 32 elements of K each
+                        mma_i8_pair(d_tmem, da + (uint64_t)((kk >> 2) * (kAtomBytes >> 4) + (kk & 3) * 2),
+                                    db + (uint64_t)((kk >> 2) * b_atom16 + (uint32_t)(kk & 3) * 2), idesc,
                                     (kb | kk) != 0 ? 1u : 0u);
-                    }
                     mma_commit_pair_multicast(&bars->empty[stage], 0x3);  // both CTAs may refill the stage
                     if (++stage == kStages) {
                         stage = 0;
@@ -291,53 +330,57 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
         }
         __syncwarp();
     } else {
-        // ---------------- epilogue: warps 2..9.  TMEM lanes are weight rows (output columns),
-        // TMEM columns activation rows: a lane's weight scale is a register, a row's scale comes from
-        // shared memory, and the 32 lanes' stores of one row are neighbours.  The next tile's scales
-        // are fetched while this one is drained.
-        const int ew = warp - 2;
+        // ---------------- epilogue: warps 2..17, in two groups of eight that take the pair's tiles in
+        // turn (one accumulator each), so that one group's stores overlap the other's arithmetic; a
+        // pair with one tile at most shares it among both.  TMEM lanes are weight rows (output
+        // columns), TMEM columns activation rows: a lane's weight scale is a register, a row's scale
+        // comes from shared memory, and the 32 lanes' stores of one row are neighbours.  The next
+        // tile's scales are fetched while this one is drained.
+        const int ew = (warp - 2) & (kEpiWarps - 1), group = (warp - 2) / kEpiWarps;
         const int quad = warp & 3;  // TMEM lane quarter this warp may read
-        const int half = ew >> 2;   // this warp takes the 32-row chunks c with c % 2 == half
+        const bool share = total_tiles <= npairs;
+        // this warp takes the chunks c = c0, c0 + cs, ... of kChunk columns
+        const int c0 = (ew >> 2) + (share ? 2 * group : 0), cs = share ? 4 : 2;
+        const int step = share ? npairs : kEpiGroups * npairs;
         const uint32_t acc_empty0[2] = {map_to_cta(smem_u32(&bars->acc_empty[0]), 0),
                                         map_to_cta(smem_u32(&bars->acc_empty[1]), 0)};
-        float* s_xs = reinterpret_cast<float*>(sEpi + (size_t)ew * kEpiBytes);
-        float* s_pr = s_xs + kWarpCols;
-        const bool has_pr = kMode == kGateUp && p.route_probs != nullptr;
-        int4 ti_next = make_int4(0, 0, 0, 0);
-        float xs_next[4], pr_next[4], ws_next = 0.0f;
+        float* s_xs = reinterpret_cast<float*>(sEpi + (size_t)(warp - 2) * kEpiBytes);
         auto first_row = [&](int t) {  // this warp's first weight row in tile t
             return (t % p.n_tiles) * kPairM + 128 * (int)rank + 32 * quad;
         };
-        auto fetch = [&](int t) {
+        auto tile_at = [&](int t) {
+            return t < total_tiles ? tile_of<kMode>(p, t / p.n_tiles, rows) : make_int4(0, 0, 0, 0);
+        };
+        float xs_next[4], ws_next = 0.0f;
+        auto fetch = [&](int t, int4 ti) {  // scales of tile t: lane l holds its rows l, l + 32, ... of this warp
             if (t >= total_tiles) return;
-            ti_next = tile_of<kMode>(p, t / p.n_tiles, rows);
             const int w = first_row(t) + lane;
             if (kMode == kGateUp || w < p.out_cols)
-                ws_next = __ldg(p.w_scale + (kMode == kDense ? 0 : (size_t)ti_next.x * p.a_rows) + w);
+                ws_next = __ldg(p.w_scale + (kMode == kDense ? 0 : (size_t)ti.x * p.a_rows) + w);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = (half + 2 * i) * 32 + lane;
-                xs_next[i] = r < ti_next.z ? __ldg(p.row_scale + ti_next.y + r) : 0.0f;
-                if (has_pr) pr_next[i] = r < ti_next.z ? __ldg(p.route_probs + __ldg(p.perm + ti_next.w + r)) : 0.0f;
+                const int r = (c0 + (2 * i + (lane >> 4)) * cs) * kChunk + (lane & 15);
+                xs_next[i] = r < ti.z ? __ldg(p.row_scale + ti.y + r) : 0.0f;
             }
         };
-        fetch(pair);
-        int it = 0;
-        for (int t = pair; t < total_tiles; t += npairs, ++it) {
+        const int t_first = pair + (share ? 0 : group * npairs);
+        int4 ti_next = tile_at(t_first), ti_after = tile_at(t_first + step);
+        fetch(t_first, ti_next);
+        int it = share ? 0 : group;
+        for (int t = t_first; t < total_tiles; t += step, it += share ? 1 : kEpiGroups) {
             const int buf = it & 1;
             const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
             const int4 ti = ti_next;
             const float ws = ws_next;
-            const int nch = tile_n(ti.z) >> 5;
+            const int nch = tile_n(ti.z) / kChunk;
             const int w0 = first_row(t);
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                s_xs[i * 32 + lane] = xs_next[i];
-                if (has_pr) s_pr[i * 32 + lane] = pr_next[i];
-            }
+            for (int i = 0; i < 4; ++i) s_xs[i * 32 + lane] = xs_next[i];
             __syncwarp();
-            fetch(t + npairs);
+            ti_next = ti_after;
+            fetch(t + step, ti_next);
+            ti_after = tile_at(t + 2 * step);
             const bool got = __all_sync(0xffffffffu,
                                         mbar_wait_bounded(&bars->acc_full[buf], acc_phase, abort_flag, p.wait_limit_ns));
             if (!got) {
@@ -349,76 +392,74 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
             const int f0 = p.relu2 ? w0 : w0 >> 1;  // gate/up: first of this warp's 32 (16) f
             const bool cols = (kMode == kGateUp ? f0 : w0) < p.out_cols;
 #pragma unroll 1
-            for (int c = half; c < nch; c += 2) {
-                uint32_t v[32];
-                tmem_ld_32x32b_x32(taddr + c * 32, v);
+            for (int c = c0, i = 0; c < nch; c += cs, ++i) {
+                uint32_t v[kChunk];
+                tmem_ld_32x32b_x16(taddr + c * kChunk, v);
+                float pv = 1.0f;  // gate/up with probabilities: lane l holds row l's
+                if (kMode == kGateUp && p.route_probs != nullptr && c * kChunk + (lane & 15) < ti.z)
+                    pv = __ldg(p.route_probs + __ldg(p.perm + ti.w + c * kChunk + (lane & 15)));
                 tmem_ld_wait();
-                if (c + 2 >= nch) {  // the last of this warp's columns is in registers
+                if (c + cs >= nch) {  // the last of this warp's columns is in registers
                     tc_fence_before_sync();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty0[buf]);
                 }
                 if (!cols) continue;
-                const float4* xs4 = reinterpret_cast<const float4*>(s_xs + (c >> 1) * 32);
-                float g[32];
+                const float4* xs4 = reinterpret_cast<const float4*>(s_xs + i * kChunk);
+                float g[kChunk];
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
+                for (int q = 0; q < kChunk / 4; ++q) {
                     const float4 xs = xs4[q];
                     g[4 * q] = __int2float_rn((int)v[4 * q]) * xs.x * ws;
                     g[4 * q + 1] = __int2float_rn((int)v[4 * q + 1]) * xs.y * ws;
                     g[4 * q + 2] = __int2float_rn((int)v[4 * q + 2]) * xs.z * ws;
                     g[4 * q + 3] = __int2float_rn((int)v[4 * q + 3]) * xs.w * ws;
                 }
-                const int left = ti.z - c * 32;  // rows of this chunk that exist (may be more than 32)
+                // rows of this chunk that exist; a whole chunk is stored without asking row by row
+                // (branches around each store cost a quarter of the epilogue's time)
+                const int left = ti.z - c * kChunk;
                 if (kMode == kGateUp) {
                     __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(p.out) +
-                                       (size_t)(ti.y + c * 32) * (size_t)p.out_ld + f0;
-                    const float* pr = s_pr + (c >> 1) * 32;
+                                       (size_t)(ti.y + c * kChunk) * (size_t)p.out_ld + f0;
                     if (p.clamp > 0.0f) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) g[j] = clamp_nan(g[j], p.clamp);
+                        for (int j = 0; j < kChunk; ++j) g[j] = clamp_nan(g[j], p.clamp);
                     }
                     if (p.relu2) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
+                        for (int j = 0; j < kChunk; ++j) {
                             const float r = g[j] > 0.0f || g[j] != g[j] ? g[j] : 0.0f;  // a NaN row stays NaN
-                            float hv = r * r;
-                            if (has_pr) hv *= pr[j];
-                            if (j < left) h[(size_t)j * (size_t)p.out_ld + lane] = __float2bfloat16_rn(hv);
+                            g[j] = r * r;
+                            if (p.route_probs != nullptr) g[j] *= __shfl_sync(0xffffffffu, pv, j);
                         }
+                        store_rows<kChunk>(h + lane, p.out_ld, g, left);
                     } else {
-                        // lanes < 16 hold gate, the others up of the same f: lanes < 16 keep rows 0..15
-                        // and receive their up values, the others keep rows 16..31 and receive gate.
-                        // silu(g) * u = g * u / (1 + exp(-g)), and the product does not ask which is which
+                        // lanes < 16 hold gate, the others up of the same f: lanes < 16 keep the chunk's
+                        // first rows and receive their up values, the others keep its last rows and
+                        // receive gate.  silu(g) * u = g * u / (1 + exp(-g)): the product needs no order
+                        constexpr int kHalf = kChunk / 2;
                         const bool lo = lane < 16;
-                        const int r0 = lo ? 0 : 16;
-                        __nv_bfloat16* dst = h + (size_t)r0 * (size_t)p.out_ld + (lane & 15);
+                        const int r0 = lo ? 0 : kHalf;
+                        float hv[kHalf];
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            const float mine = lo ? g[j] : g[16 + j];
-                            const float other = __shfl_xor_sync(0xffffffffu, lo ? g[16 + j] : g[j], 16);
-                            const float gate = lo ? mine : other;
-                            float hv = __fdividef(mine * other, 1.0f + __expf(-gate));
-                            if (has_pr) hv *= pr[r0 + j];
-                            if (r0 + j < left) dst[(size_t)j * (size_t)p.out_ld] = __float2bfloat16_rn(hv);
+                        for (int j = 0; j < kHalf; ++j) {
+                            const float mine = lo ? g[j] : g[kHalf + j];
+                            const float other = __shfl_xor_sync(0xffffffffu, lo ? g[kHalf + j] : g[j], 16);
+                            hv[j] = mine * other * sigmoid_approx(lo ? mine : other);
+                            if (p.route_probs != nullptr) hv[j] *= __shfl_sync(0xffffffffu, pv, r0 + j);
                         }
+                        store_rows<kHalf>(h + (size_t)r0 * (size_t)p.out_ld + (lane & 15), p.out_ld, hv,
+                                          left >= kChunk ? kHalf : left - r0);
                     }
                 } else if (w0 + lane < p.out_cols) {
-                    const size_t at = (size_t)(ti.y + c * 32) * (size_t)p.out_ld + w0 + lane;
-                    if (kMode == kDense && p.out_bf16 != 0) {
-                        __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < left) dst[(size_t)j * (size_t)p.out_ld] = __float2bfloat16_rn(g[j]);
-                    } else {
-                        float* dst = reinterpret_cast<float*>(p.out) + at;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (j < left) dst[(size_t)j * (size_t)p.out_ld] = g[j];
-                    }
+                    const size_t at = (size_t)(ti.y + c * kChunk) * (size_t)p.out_ld + w0 + lane;
+                    if (kMode == kDense && p.out_bf16 != 0)
+                        store_rows<kChunk>(reinterpret_cast<__nv_bfloat16*>(p.out) + at, p.out_ld, g, left);
+                    else
+                        store_rows<kChunk>(reinterpret_cast<float*>(p.out) + at, p.out_ld, g, left);
                 }
             }
-            if (nch <= half && lane == 0) mbar_arrive_cluster_relaxed(acc_empty0[buf]);  // no column of this warp
+            if (nch <= c0 && lane == 0) mbar_arrive_cluster_relaxed(acc_empty0[buf]);  // no column of this warp
         }
     }
 
