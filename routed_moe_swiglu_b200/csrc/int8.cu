@@ -10,6 +10,7 @@
 // bf16 weights do; padding (K past H or F, rows past F or H) holds code 0 and
 // scale 0.  Each weight row's scale stands at the row's own place in [E][rows].
 #include <cmath>
+#include <type_traits>
 
 #include "int8.cuh"
 #include "mxfp8.cuh"
@@ -20,8 +21,9 @@ namespace {
 constexpr int kI8Threads = 128;
 
 // A row is taken by kWarps warps, which hold up to kHeld 16-byte chunks a lane: one read of the
-// row serves its largest magnitude and its codes.  Longer rows read the rest twice.
-constexpr int kHeld = 8;
+// row serves its largest magnitude and its codes.  Rows longer than the most held read the rest
+// twice.
+constexpr int kMostHeld = 8;
 
 template <int kWarps>
 __device__ __forceinline__ uint32_t row_max(uint32_t a, uint32_t* s_red) {
@@ -40,7 +42,7 @@ __device__ __forceinline__ uint32_t row_max(uint32_t a, uint32_t* s_red) {
 
 // Quantises the row of `chunks` 16-byte chunks at src (none when !on): store(c, codes) for each
 // chunk; returns the scale.  Every thread of the row's warps calls it (with kWarps > 1, of the block).
-template <int kWarps, class Store>
+template <int kWarps, int kHeld, class Store>
 __device__ __forceinline__ float quantize_row(const uint4* src, int chunks, bool on, uint32_t* s_red, Store store) {
     constexpr int kLanes = kWarps * 32;
     const int lane = threadIdx.x & (kLanes - 1);
@@ -67,8 +69,8 @@ __device__ __forceinline__ float quantize_row(const uint4* src, int chunks, bool
 }
 
 // Rows of bf16, kWarps warps a row.
-template <int kWarps>
-__global__ void __launch_bounds__(kI8Threads, 6) int8_quantize_rows_kernel(const uint4* __restrict__ in, long long rows,
+template <int kWarps, int kHeld>
+__global__ void __launch_bounds__(kI8Threads, kHeld > 4 ? 6 : 10) int8_quantize_rows_kernel(const uint4* __restrict__ in, long long rows,
                                                                         int chunks, long long ld_chunks,
                                                                         const int* __restrict__ live,
                                                                         uint2* __restrict__ q,
@@ -85,7 +87,7 @@ __global__ void __launch_bounds__(kI8Threads, 6) int8_quantize_rows_kernel(const
     for (long long r0 = (long long)blockIdx.x * kRows; r0 < n; r0 += (long long)gridDim.x * kRows) {
         const long long r = r0 + threadIdx.x / (kWarps * 32);
         const bool on = r < n;
-        const float s = quantize_row<kWarps>(in + r * ld_chunks, chunks, on, s_red,
+        const float s = quantize_row<kWarps, kHeld>(in + r * ld_chunks, chunks, on, s_red,
                                              [&](int c, uint2 codes) { q[r * chunks + c] = codes; });
         if (on && (threadIdx.x & (kWarps * 32 - 1)) == 0) scales[r] = s;
     }
@@ -93,6 +95,7 @@ __global__ void __launch_bounds__(kI8Threads, 6) int8_quantize_rows_kernel(const
 
 // x rows: a block per token writes the token's codes and scale to each of its k padded route
 // rows (zero codes from H to the pitch hp).
+template <int kHeld>
 __global__ void __launch_bounds__(kI8Threads) gather_rows_int8_kernel(const uint4* __restrict__ x,
                                                                       const int* __restrict__ live, int max_live,
                                                                       int H, int hp, int k,
@@ -115,7 +118,7 @@ __global__ void __launch_bounds__(kI8Threads) gather_rows_int8_kernel(const uint
                 if (pr >= 0) xq[(size_t)pr * chunks_out + c] = codes;
             }
         };
-        const float s = quantize_row<kI8Threads / 32>(x + (size_t)t * chunks, chunks, true, s_red, put);
+        const float s = quantize_row<kI8Threads / 32, kHeld>(x + (size_t)t * chunks, chunks, true, s_red, put);
         if (threadIdx.x < k && s_prow[threadIdx.x] >= 0) xs[s_prow[threadIdx.x]] = s;
         for (int c = chunks + threadIdx.x; c < chunks_out; c += kI8Threads) put(c, make_uint2(0u, 0u));
     }
@@ -123,8 +126,8 @@ __global__ void __launch_bounds__(kI8Threads) gather_rows_int8_kernel(const uint
 
 // h rows: kWarps warps per live route quantise its bf16 row of the gate/up GEMM (pitch fp, zeros
 // past F) with the row's own scale.
-template <int kWarps>
-__global__ void __launch_bounds__(kI8Threads, 6) quantize_h_int8_kernel(const uint4* __restrict__ h,
+template <int kWarps, int kHeld>
+__global__ void __launch_bounds__(kI8Threads, kHeld > 4 ? 6 : 10) quantize_h_int8_kernel(const uint4* __restrict__ h,
                                                                      const int* __restrict__ live, int max_live,
                                                                      int k, int fp, const int* __restrict__ inv,
                                                                      uint2* __restrict__ hq, float* __restrict__ hs,
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__(kI8Threads, 6) quantize_h_int8_kernel(const ui
     for (long long i0 = (long long)blockIdx.x * kRows; i0 < n; i0 += (long long)gridDim.x * kRows) {
         const long long i = i0 + threadIdx.x / (kWarps * 32);
         const int pr = i < n ? __ldg(inv + i) : -1;
-        const float s = quantize_row<kWarps>(h + (size_t)(pr < 0 ? 0 : pr) * chunks, chunks, pr >= 0, s_red,
+        const float s = quantize_row<kWarps, kHeld>(h + (size_t)(pr < 0 ? 0 : pr) * chunks, chunks, pr >= 0, s_red,
                                              [&](int c, uint2 codes) { hq[(size_t)pr * chunks + c] = codes; });
         if (pr >= 0 && (threadIdx.x & (kWarps * 32 - 1)) == 0) hs[pr] = s;
     }
@@ -173,7 +176,7 @@ __global__ void __launch_bounds__(kI8Threads) prepare_int8_kernel(
         const int chunks = (first ? H : F) / 8, atoms = first ? at1 : at2, per = first ? w1r : hr;
         const long long grow = e * per + wrow;
         uint2* dst = (first ? w1q : w2q) + ((size_t)(grow >> 7) * atoms * 128 + (grow & 127)) * 16;
-        const float s = quantize_row<kI8Threads / 32>(src, chunks, true, s_red, [&](int c, uint2 codes) {
+        const float s = quantize_row<kI8Threads / 32, kMostHeld>(src, chunks, true, s_red, [&](int c, uint2 codes) {
             dst[(size_t)(c >> 4) * (128 * 16) + (c & 15)] = codes;
         });
         if (threadIdx.x == 0) (first ? w1s : w2s)[grow] = s;
@@ -246,37 +249,51 @@ size_t linear_scales_offset(long long rows, int cols_in) {
 // Whether `rows` rows of `chunks` 16-byte chunks are taken by a warp each: rows a warp can hold,
 // and enough of them to fill the SMs; else a block of four warps takes one.
 static bool warp_per_row(long long rows, int chunks) {
-    return chunks <= kHeld * 32 && rows >= (long long)num_sms() * 16;
+    return chunks <= kMostHeld * 32 && rows >= (long long)num_sms() * 16;
+}
+
+// Calls f with the warps a row gets and the chunks a lane holds (2, 4 or 8) as constants.
+template <class F>
+static cudaError_t by_row(bool warp, int chunks, F f) {
+    const int need = (chunks + (warp ? 31 : 127)) / (warp ? 32 : 128);
+    auto held = [&](auto warps) {
+        if (need <= 2) return f(warps, std::integral_constant<int, 2>());
+        if (need <= 4) return f(warps, std::integral_constant<int, 4>());
+        return f(warps, std::integral_constant<int, kMostHeld>());
+    };
+    return warp ? held(std::integral_constant<int, 1>()) : held(std::integral_constant<int, 4>());
 }
 
 cudaError_t launch_int8_quantize_rows(const __nv_bfloat16* in, long long rows, int cols, long long ld_in, int8_t* q,
                                       float* scales, const int* live, cudaStream_t s) {
-    const uint4* src = reinterpret_cast<const uint4*>(in);
-    uint2* dst = reinterpret_cast<uint2*>(q);
-    if (warp_per_row(rows, cols / 8))
-        return launch_dependent(int8_quantize_rows_kernel<1>, dim3(capped_grid((rows + 3) / 4, 16)), dim3(kI8Threads), 0,
-                                s, src, rows, cols / 8, ld_in / 8, live, dst, scales);
-    return launch_dependent(int8_quantize_rows_kernel<4>, dim3(capped_grid(rows, 16)), dim3(kI8Threads), 0, s, src, rows,
-                            cols / 8, ld_in / 8, live, dst, scales);
+    return by_row(warp_per_row(rows, cols / 8), cols / 8, [&](auto warps, auto held) {
+        constexpr int kRows = 4 / warps.value;
+        return launch_dependent(int8_quantize_rows_kernel<warps.value, held.value>,
+                                dim3(capped_grid((rows + kRows - 1) / kRows, 16)), dim3(kI8Threads), 0, s,
+                                reinterpret_cast<const uint4*>(in), rows, cols / 8, ld_in / 8, live,
+                                reinterpret_cast<uint2*>(q), scales);
+    });
 }
 
 cudaError_t launch_gather_int8(const __nv_bfloat16* x, const int* live, int max_live, int H, int hp, int k,
                                const int* inv, uint8_t* xq, float* xs, const unsigned* status, cudaStream_t s) {
-    return launch_dependent(gather_rows_int8_kernel, dim3(capped_grid(max_live, 16)), dim3(kI8Threads), 0, s,
-                            reinterpret_cast<const uint4*>(x), live, max_live, H, hp, k, inv,
-                            reinterpret_cast<uint2*>(xq), xs, status);
+    return by_row(false, H / 8, [&](auto, auto held) {
+        return launch_dependent(gather_rows_int8_kernel<held.value>, dim3(capped_grid(max_live, 16)),
+                                dim3(kI8Threads), 0, s, reinterpret_cast<const uint4*>(x), live, max_live, H, hp, k,
+                                inv, reinterpret_cast<uint2*>(xq), xs, status);
+    });
 }
 
 cudaError_t launch_quantize_h_int8(const __nv_bfloat16* h, const int* live, int max_live, int k, int fp,
                                    const int* inv, uint8_t* hq, float* hs, const unsigned* status, cudaStream_t s) {
     const long long rows = (long long)max_live * k;
-    const uint4* src = reinterpret_cast<const uint4*>(h);
-    uint2* dst = reinterpret_cast<uint2*>(hq);
-    if (warp_per_row(rows, fp / 8))
-        return launch_dependent(quantize_h_int8_kernel<1>, dim3(capped_grid((rows + 3) / 4, 16)), dim3(kI8Threads), 0, s,
-                                src, live, max_live, k, fp, inv, dst, hs, status);
-    return launch_dependent(quantize_h_int8_kernel<4>, dim3(capped_grid(rows, 16)), dim3(kI8Threads), 0, s, src, live,
-                            max_live, k, fp, inv, dst, hs, status);
+    return by_row(warp_per_row(rows, fp / 8), fp / 8, [&](auto warps, auto held) {
+        constexpr int kRows = 4 / warps.value;
+        return launch_dependent(quantize_h_int8_kernel<warps.value, held.value>,
+                                dim3(capped_grid((rows + kRows - 1) / kRows, 16)), dim3(kI8Threads), 0, s,
+                                reinterpret_cast<const uint4*>(h), live, max_live, k, fp, inv,
+                                reinterpret_cast<uint2*>(hq), hs, status);
+    });
 }
 
 cudaError_t launch_prepare_int8(const moe_plan* p, const __nv_bfloat16* wg, const __nv_bfloat16* wu,
