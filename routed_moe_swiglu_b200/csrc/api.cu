@@ -472,6 +472,7 @@ static moe_status forward_impl(const moe_plan* plan, const void* x, const float*
         g.status_words = status;
         g.status_flags = status + kStFlags;
         g.wait_limit_ns = kWaitLimitNs;
+        g.early = 1;  // the gather and the pass over h release their GEMM after their own wait
         g.perm = perm;
         g.out = ws + L.hf;
         g.out_ld = g.out_cols = (int)plan->fp;

@@ -191,7 +191,10 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
     cluster_sync();  // both CTAs' barriers and TMEM exist before any cross-CTA traffic
     tc_fence_after_sync();
     const uint32_t tmem_base = bars->tmem_base;
-    pdl_wait();
+    // `early`: the kernel before this one let it start only once all that came before that kernel
+    // was done.  Sizes, tiles and weights then need no wait, and the first stages' weights are on
+    // their way while that kernel still writes this one's activation rows.
+    if (!p.early) pdl_wait();
 
     int num_m, rows = 0, widest;
     if (kMode == kDense) {
@@ -208,6 +211,7 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
     const int kStages = sc.n;
     const uint32_t kBBytes = sc.b;
     uint8_t* sB = smem + kStages * kABytes;
+    if (p.early && warp != 0) pdl_wait();
     auto timed_out = [&]() {
         *abort_flag = 1;
         if (p.status_flags != nullptr) atomicOr(p.status_flags, MOE_DEV_TIMEOUT);
@@ -222,41 +226,79 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
             bool ok = true;
             int last_phase[kStagesMax];
             for (int s = 0; s < kStagesMax; ++s) last_phase[s] = -1;
-            int4 ti_n = total_tiles > pair ? tile_of<kMode>(p, pair / p.n_tiles, rows) : make_int4(0,0,0,0);
+            // Experts with one route tile each (decode): every weight tile is read once; its lines go
+            // first out of L2, which keeps the rows that the next kernels read there.
+            const bool weights_once = kMode != kDense && widest < kRouteTile;
+            const uint64_t pol_once = l2_policy_evict_first();
+            auto weights = [&](int s, int e, int w_row, int kb) {  // K stage kb of 128 weight rows into stage s
+                const uint32_t full0 = map_to_cta(smem_u32(&bars->full[s]), 0);
+                uint8_t* dst = sA + s * kABytes;
+                if (kMode == kDense) {
+                    // atoms of plain rows; columns from K on are filled with zeros
+#pragma unroll
+                    for (int at = 0; at < kAtoms; ++at)
+                        tma_load_2d_pair(dst + at * kAtomBytes, &tmA, full0, (kb * kAtoms + at) * 128, w_row);
+                } else {
+                    const int atom = (int)(((long long)e * p.a_rows + w_row) / 128 * p.atoms) + kb * kAtoms;
+                    if (weights_once)
+                        tma_load_3d_pair_hint(dst, &tmA, full0, 0, 0, atom, pol_once);
+                    else
+                        tma_load_3d_pair(dst, &tmA, full0, 0, 0, atom);
+                }
+            };
+            auto stage_bytes = [&](int z) {  // both CTAs' loads of a stage of a tile of z rows
+                return 2u * (kABytes + (uint32_t)(tile_n(z) >> 1) * (kAtoms * 128u));
+            };
+            int pre = 0;  // stages whose weights are requested before the wait
+            if (p.early) {
+                int kb = 0;
+                for (int t = pair; t < total_tiles && pre < kStages;) {
+                    const int4 ti = tile_of<kMode>(p, t / p.n_tiles, rows);
+                    if (leader) {
+                        mbar_arrive_expect_tx(&bars->full[pre], stage_bytes(ti.z));
+                        last_phase[pre] = 0;
+                    }
+                    weights(pre, ti.x, t % p.n_tiles * kPairM + 128 * (int)rank, kb);
+                    ++pre;
+                    if (++kb == kb_count) {
+                        kb = 0;
+                        t += npairs;
+                    }
+                }
+                pdl_wait();
+            }
+            int4 ti_n = total_tiles > pair ? tile_of<kMode>(p, pair / p.n_tiles, rows) : make_int4(0, 0, 0, 0);
             for (int t = pair; t < total_tiles && ok; t += npairs) {
                 const int mt = t / p.n_tiles, nt = t - mt * p.n_tiles;
                 const int4 ti = ti_n;
                 if (t + npairs < total_tiles) ti_n = tile_of<kMode>(p, (t + npairs) / p.n_tiles, rows);
                 const int hb = tile_n(ti.z) >> 1;
-                const uint32_t tx = 2u * (kABytes + (uint32_t)hb * (kAtoms * 128u));
+                const uint32_t tx = stage_bytes(ti.z);
                 const CUtensorMap* mb = &tmB->m[(hb >> 4) - 1];
                 const int w_row = nt * kPairM + 128 * (int)rank;
-                const int a_atom0 = kMode == kDense
-                                        ? 0
-                                        : (int)(((long long)ti.x * p.a_rows + w_row) / 128 * p.atoms);
                 const int b_row = ti.y + hb * (int)rank;
                 for (int kb = 0; kb < kb_count; ++kb) {
-                    if (!mbar_wait_bounded(&bars->empty[stage], phase ^ 1u, abort_flag, p.wait_limit_ns)) {
-                        ok = false;
-                        break;
+                    if (pre > 0) {
+                        --pre;
+                    } else {
+                        if (!mbar_wait_bounded(&bars->empty[stage], phase ^ 1u, abort_flag, p.wait_limit_ns)) {
+                            ok = false;
+                            break;
+                        }
+                        if (leader) {
+                            mbar_arrive_expect_tx(&bars->full[stage], tx);
+                            last_phase[stage] = (int)phase;
+                        }
+                        weights(stage, ti.x, w_row, kb);
                     }
                     const uint32_t full0 = map_to_cta(smem_u32(&bars->full[stage]), 0);
-                    if (leader) {
-                        mbar_arrive_expect_tx(&bars->full[stage], tx);
-                        last_phase[stage] = (int)phase;
-                    }
-                    uint8_t* a_dst = sA + stage * kABytes;
                     uint8_t* b_dst = sB + stage * kBBytes;
                     if (kMode == kDense) {
-                        // atoms of plain rows; columns from K on are filled with zeros
 #pragma unroll
-                        for (int at = 0; at < kAtoms; ++at) {
-                            const int k0 = (kb * kAtoms + at) * 128;
-                            tma_load_2d_pair(a_dst + at * kAtomBytes, &tmA, full0, k0, w_row);
-                            tma_load_2d_pair(b_dst + (uint32_t)at * (uint32_t)hb * 128u, mb, full0, k0, b_row);
-                        }
+                        for (int at = 0; at < kAtoms; ++at)
+                            tma_load_2d_pair(b_dst + (uint32_t)at * (uint32_t)hb * 128u, mb, full0,
+                                             (kb * kAtoms + at) * 128, b_row);
                     } else {
-                        tma_load_3d_pair(a_dst, &tmA, full0, 0, 0, a_atom0 + kb * kAtoms);
                         tma_load_3d_pair(b_dst, mb, full0, 0, b_row, kb * kAtoms);
                     }
                     if (++stage == kStages) {
@@ -285,6 +327,7 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
             uint32_t phase = 0;
             bool ok = true;
             int it = 0;
+            // rows of the next tile, fetched ahead
             int zn = total_tiles > pair ? tile_of<kMode>(p, pair / p.n_tiles, rows).z : 0;
             for (int t = pair; t < total_tiles && ok; t += npairs, ++it) {
                 const int buf = it & 1;

@@ -41,9 +41,11 @@ __device__ __forceinline__ uint32_t row_max(uint32_t a, uint32_t* s_red) {
 }
 
 // Quantises the row of `chunks` 16-byte chunks at src (none when !on): store(c, codes) for each
-// chunk; returns the scale.  Every thread of the row's warps calls it (with kWarps > 1, of the block).
-template <int kWarps, int kHeld, class Store>
-__device__ __forceinline__ float quantize_row(const uint4* src, int chunks, bool on, uint32_t* s_red, Store store) {
+// chunk, after ready(); returns the scale.  Every thread of the row's warps calls it (with kWarps
+// > 1, of the block).
+template <int kWarps, int kHeld, class Ready, class Store>
+__device__ __forceinline__ float quantize_row(const uint4* src, int chunks, bool on, uint32_t* s_red, Ready ready,
+                                              Store store) {
     constexpr int kLanes = kWarps * 32;
     const int lane = threadIdx.x & (kLanes - 1);
     uint4 v[kHeld];
@@ -58,6 +60,7 @@ __device__ __forceinline__ float quantize_row(const uint4* src, int chunks, bool
     if (on)
         for (int c = kHeld * kLanes + lane; c < chunks; c += kLanes) a = int8_amax_pairs(__ldg(src + c), a);
     const Int8Row row = int8_row(__uint_as_float(row_max<kWarps>(int8_amax_bits(a), s_red)));
+    ready();
 #pragma unroll
     for (int i = 0; i < kHeld; ++i) {
         const int c = i * kLanes + lane;
@@ -87,8 +90,8 @@ __global__ void __launch_bounds__(kI8Threads, kHeld > 4 ? 6 : 10) int8_quantize_
     for (long long r0 = (long long)blockIdx.x * kRows; r0 < n; r0 += (long long)gridDim.x * kRows) {
         const long long r = r0 + threadIdx.x / (kWarps * 32);
         const bool on = r < n;
-        const float s = quantize_row<kWarps, kHeld>(in + r * ld_chunks, chunks, on, s_red,
-                                             [&](int c, uint2 codes) { q[r * chunks + c] = codes; });
+        const float s = quantize_row<kWarps, kHeld>(in + r * ld_chunks, chunks, on, s_red, [] {},
+                                                    [&](int c, uint2 codes) { q[r * chunks + c] = codes; });
         if (on && (threadIdx.x & (kWarps * 32 - 1)) == 0) scales[r] = s;
     }
 }
@@ -104,24 +107,38 @@ __global__ void __launch_bounds__(kI8Threads) gather_rows_int8_kernel(const uint
                                                                       const unsigned* status) {
     __shared__ int s_prow[kMaxTopK];
     __shared__ uint32_t s_red[kI8Threads / 32];
-    pdl_trigger();
-    pdl_wait();
-    const int n = live_rows(live, max_live, status);
+    // The permute before this kernel releases it after its own wait, so x and the live count are
+    // there: the first row's codes are computed before this kernel waits for the permutation.  The
+    // gate/up GEMM is released after that wait (its `early`).
+    const int n = clamp_live(live, max_live);
     const int chunks = H / 8, chunks_out = hp / 8;
-    for (int t = blockIdx.x; t < n; t += gridDim.x) {
-        __syncthreads();
-        if (threadIdx.x < k) s_prow[threadIdx.x] = __ldg(inv + (size_t)t * k + threadIdx.x);
-        // (the barriers of the row's maximum order s_prow before its readers)
+    bool waited = false, go = true;
+    auto wait = [&] {
+        if (!waited) {
+            pdl_wait();
+            pdl_trigger();
+            go = !forward_poisoned(status);
+            waited = true;
+        }
+    };
+    for (int t = blockIdx.x; t < n && go; t += gridDim.x) {
+        auto ready = [&] {
+            wait();
+            __syncthreads();  // the last token's readers of s_prow are done
+            if (threadIdx.x < k) s_prow[threadIdx.x] = go ? __ldg(inv + (size_t)t * k + threadIdx.x) : -1;
+            __syncthreads();
+        };
         auto put = [&](int c, uint2 codes) {
             for (int j = 0; j < k; ++j) {
                 const int pr = s_prow[j];
                 if (pr >= 0) xq[(size_t)pr * chunks_out + c] = codes;
             }
         };
-        const float s = quantize_row<kI8Threads / 32, kHeld>(x + (size_t)t * chunks, chunks, true, s_red, put);
+        const float s = quantize_row<kI8Threads / 32, kHeld>(x + (size_t)t * chunks, chunks, true, s_red, ready, put);
         if (threadIdx.x < k && s_prow[threadIdx.x] >= 0) xs[s_prow[threadIdx.x]] = s;
         for (int c = chunks + threadIdx.x; c < chunks_out; c += kI8Threads) put(c, make_uint2(0u, 0u));
     }
+    wait();  // every block, so that the kernel never ends before the permute
 }
 
 // h rows: kWarps warps per live route quantise its bf16 row of the gate/up GEMM (pitch fp, zeros
@@ -134,15 +151,15 @@ __global__ void __launch_bounds__(kI8Threads, kHeld > 4 ? 6 : 10) quantize_h_int
                                                                      const unsigned* status) {
     constexpr int kRows = kI8Threads / 32 / kWarps;
     __shared__ uint32_t s_red[kI8Threads / 32];
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();  // after the wait: the down GEMM's `early`
     const long long n = (long long)live_rows(live, max_live, status) * k;
     const int chunks = fp / 8;
     for (long long i0 = (long long)blockIdx.x * kRows; i0 < n; i0 += (long long)gridDim.x * kRows) {
         const long long i = i0 + threadIdx.x / (kWarps * 32);
         const int pr = i < n ? __ldg(inv + i) : -1;
         const float s = quantize_row<kWarps, kHeld>(h + (size_t)(pr < 0 ? 0 : pr) * chunks, chunks, pr >= 0, s_red,
-                                             [&](int c, uint2 codes) { hq[(size_t)pr * chunks + c] = codes; });
+                                                    [] {}, [&](int c, uint2 codes) { hq[(size_t)pr * chunks + c] = codes; });
         if (pr >= 0 && (threadIdx.x & (kWarps * 32 - 1)) == 0) hs[pr] = s;
     }
 }
@@ -176,7 +193,7 @@ __global__ void __launch_bounds__(kI8Threads) prepare_int8_kernel(
         const int chunks = (first ? H : F) / 8, atoms = first ? at1 : at2, per = first ? w1r : hr;
         const long long grow = e * per + wrow;
         uint2* dst = (first ? w1q : w2q) + ((size_t)(grow >> 7) * atoms * 128 + (grow & 127)) * 16;
-        const float s = quantize_row<kI8Threads / 32, kMostHeld>(src, chunks, true, s_red, [&](int c, uint2 codes) {
+        const float s = quantize_row<kI8Threads / 32, kMostHeld>(src, chunks, true, s_red, [] {}, [&](int c, uint2 codes) {
             dst[(size_t)(c >> 4) * (128 * 16) + (c & 15)] = codes;
         });
         if (threadIdx.x == 0) (first ? w1s : w2s)[grow] = s;
@@ -207,7 +224,7 @@ moe_status check_product(long long rows, int cols_in, const void* w, const float
 
 moe_status run_dense(const int8_t* x, const float* x_scales, long long rows, int cols_in, long long ld_x,
                      const int8_t* w, const float* w_scales, int cols_out, void* out, long long ld_out, int out_bf16,
-                     const int* live, unsigned* status, cudaStream_t s) {
+                     const int* live, unsigned* status, bool early, cudaStream_t s) {
     CUtensorMap tA;
     BoxMaps8 tB;
     // rows of K bytes; columns past K and rows past the last read as zero
@@ -236,6 +253,7 @@ moe_status run_dense(const int8_t* x, const float* x_scales, long long rows, int
     g.live = live;
     g.rows = (int)rows;
     g.out_bf16 = out_bf16;
+    g.early = early;
     const long long tiles = (rows + kRouteTile - 1) / kRouteTile * g.n_tiles;
     return launch_gemm_dense_int8(tA, tB, g, tiles, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -340,7 +358,7 @@ moe_status int8_matmul(const int8_t* x, const float* x_scales, long long rows, i
         return MOE_ERR_ALIGNMENT;
     if (rows == 0) return MOE_OK;
     return run_dense(x, x_scales, rows, cols_in, ld_x, w, w_scales, cols_out, out, ld_out, out_bf16, live_rows_dev,
-                     status_dev, static_cast<cudaStream_t>(stream));
+                     status_dev, false, static_cast<cudaStream_t>(stream));
 }
 
 size_t int8_linear_workspace_bytes(long long rows, int cols_in) {
@@ -366,7 +384,7 @@ moe_status int8_linear(const void* x, long long rows, int cols_in, long long ld_
                                   s) != cudaSuccess)
         return MOE_ERR_CUDA;
     return run_dense(q, scales, rows, cols_in, cols_in, w, w_scales, cols_out, out, ld_out, out_bf16, live_rows_dev,
-                     status_dev, s);
+                     status_dev, true, s);
 }
 
 }  // extern "C"

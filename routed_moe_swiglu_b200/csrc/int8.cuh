@@ -113,6 +113,7 @@ struct Int8Gemm {
     const int* live;                // null: all rows
     int rows;
     int out_bf16;
+    int early;                      // launched by a kernel that waited before it released this one
 };
 
 cudaError_t launch_gemm1_int8(const CUtensorMap& a, const BoxMaps8& b, const Int8Gemm& g, long long max_tiles,
