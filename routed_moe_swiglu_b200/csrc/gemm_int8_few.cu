@@ -1,0 +1,411 @@
+// gemm_int8_few.cu -- the dense 8-bit product of few tokens: K is split over the
+// CTAs of a cluster.
+//
+// With few tokens the time is that of reading the weights, and a wide tile of
+// weight rows leaves most SMs without one.  Here a CTA takes 128 weight rows and
+// a slice of K, the up to eight CTAs of a cluster share a tile's K, and their
+// int32 partial sums (exact, so their order is of no account) are added through
+// distributed shared memory; each CTA finishes every S-th token.
+//
+//   kFused   up to 16 tokens of bf16: each CTA quantises its own slice of the
+//            rows into the swizzled operand layout in shared memory; the rows'
+//            largest magnitudes meet in one cluster barrier.  One launch does all.
+//   !kFused  up to 64 tokens a tile, whose codes TMA loads beside the weights.
+//
+// Roles (6 warps): warp 0 issues TMA loads, warp 1 owns TMEM and issues the MMAs
+// (tcgen05 kind::i8, M = 128), warps 2-5 quantise (kFused) and drain.  Every
+// mbarrier wait is bounded; a wait that gave up is followed by the same cluster
+// barriers as any other, so no CTA is left alone in one.
+#include "int8.cuh"
+#include "ptx.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kFewThreads = 192;
+constexpr int kWorkers = 128;              // warps 2..5
+constexpr int kFewTokens = 64;             // tokens of a tile at most
+constexpr int kFusedTokens = 16;
+constexpr int kFusedAtoms = 16;            // 128-element atoms of a K slice that kFused holds
+constexpr uint32_t kAAtom = 128 * 128;     // 128 weight rows of 128 bytes
+constexpr int kMaxCluster = 8;
+
+template <bool kFused>
+struct FewCfg {
+    static constexpr int kStages = kFused ? 4 : 3;
+    static constexpr uint32_t kBSlot = kFused ? kFusedTokens * 128 : kFewTokens * 128;  // an atom of the tokens
+    static constexpr uint32_t kBBytes = kBSlot * (kFused ? kFusedAtoms : kStages);
+    static constexpr uint32_t kPartBytes = (kFused ? kFusedTokens : kFewTokens) * 128 * 4;
+    static constexpr size_t kSmem = 1024 + kStages * kAAtom + kBBytes + kPartBytes + 512;
+};
+
+struct __align__(8) FewShared {
+    uint64_t full[4], empty[4], acc_full, b_ready;
+    uint32_t tmem_base;
+    int abort_flag;
+    uint32_t amax[kMaxCluster][kFusedTokens];  // kFused: each CTA of the cluster writes its row
+};
+
+struct FewArgs {
+    const uint4* x;          // kFused: bf16 rows
+    long long ld_x;          // their pitch, 16-byte chunks
+    const float* x_scales;   // !kFused
+    const float* w_scales;
+    void* out;
+    long long ld_out;
+    int cols_in, cols_out, rows;
+    const int* live;
+    int out_bf16, split, early;
+    unsigned* status;
+    unsigned long long wait_limit_ns;
+};
+
+__host__ __device__ constexpr uint32_t idesc_i8_cta(int N) {
+    return (2u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_i8_cta(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                           uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+
+// The two halves of cluster_sync().
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+template <bool kFused>
+__global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid_constant__ CUtensorMap tmA,
+                                                                    const __grid_constant__ BoxMaps8 tmB,
+                                                                    const FewArgs a) {
+    using C = FewCfg<kFused>;
+    constexpr int kStages = C::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ FewShared sh;
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sA = smem;
+    uint8_t* sB = sA + kStages * kAAtom;
+    int* s_part = reinterpret_cast<int*>(sB + C::kBBytes);  // [token][128 channels]
+    volatile int* abort_flag = &sh.abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int S = a.split, rank = (int)cluster_ctarank();
+    const int n0 = (int)(blockIdx.x / S) * 128;                 // first weight row (output column)
+    const int m0 = (int)blockIdx.y * kFewTokens;                // first token
+    const int atoms = (a.cols_in + kAtomK8 - 1) / kAtomK8;
+    const int k0 = (int)((long long)atoms * rank / S), k1 = (int)((long long)atoms * (rank + 1) / S);
+    const int steps = k1 - k0;                                  // at least 1: S <= atoms
+    pdl_trigger();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sh.full[s], 1);
+            mbar_init(&sh.empty[s], 1);
+        }
+        mbar_init(&sh.acc_full, 1);
+        mbar_init(&sh.b_ready, kWorkers);
+        sh.abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(&sh.tmem_base, 64);
+        tmem_relinquish();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = sh.tmem_base;
+    if (kFused) cluster_arrive();  // every CTA runs before another writes into its shared memory
+    // `early` (see gemm_int8.cu): weights and sizes need no wait
+    if (!a.early) pdl_wait();
+    const int rows = a.live != nullptr ? clamp_live(a.live, a.rows) : a.rows;
+    const int nt = min(rows - m0, kFewTokens);  // tokens of this tile
+    if (kFused) cluster_wait();
+    if (nt <= 0) {                              // the whole cluster: same tile
+        if (a.early) pdl_wait();
+        __syncthreads();
+        if (warp == 1) tmem_dealloc(tmem_base, 64);
+        return;
+    }
+    const int N = (nt + 15) & ~15;
+    const uint32_t b_atom = kFused ? C::kBSlot : (uint32_t)N * 128u;
+    auto timed_out = [&]() {
+        *abort_flag = 1;
+        if (a.status != nullptr) atomicOr(a.status, MOE_DEV_TIMEOUT);
+    };
+
+    int issued = 0, last_phase[4] = {-1, -1, -1, -1};
+    bool ok = true;
+    // step i of the slice into its stage: weights, and the tokens' codes (!kFused)
+    auto request = [&](int i, bool w, bool b) {
+        const int s = i % kStages;
+        if (w) {
+            mbar_arrive_expect_tx(&sh.full[s], kAAtom + (kFused ? 0u : b_atom));
+            last_phase[s] = (i / kStages) & 1;
+            tma_load_2d(sA + s * kAAtom, &tmA, &sh.full[s], (k0 + i) * 128, n0);
+        }
+        if (b && !kFused)
+            tma_load_2d(sB + s * C::kBSlot, &tmB.m[(N >> 4) - 1], &sh.full[s], (k0 + i) * 128, m0);
+    };
+    if (warp == 0 && lane == 0) {
+        const int first = min(steps, kStages);
+        for (int i = 0; i < first; ++i) request(i, true, false);
+        if (a.early) pdl_wait();
+        for (int i = 0; i < first; ++i) request(i, false, true);
+        issued = first;
+    } else if (a.early) {
+        pdl_wait();
+    }
+    __syncwarp();
+
+    // ---------------- kFused: worker warp w quantises rows w, w + 4, ... of the tile
+    const int wt = (int)threadIdx.x - 64;  // worker thread
+    if (kFused) {
+        constexpr int kRows = kFusedTokens / 4;
+        const int units = min(steps * 8, (a.cols_in - k0 * 128 + 15) / 16);  // 16 elements each, of a row's slice
+        const uint4* src[kRows];
+        if (wt >= 0) {
+            uint32_t p[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int r = warp - 2 + 4 * i;
+                src[i] = a.x + (size_t)(m0 + min(r, nt - 1)) * a.ld_x + (size_t)k0 * 16;
+                p[i] = 0u;
+            }
+            for (int u = lane; u < units; u += 32)
+#pragma unroll
+                for (int i = 0; i < kRows; ++i)
+                    if (warp - 2 + 4 * i < nt)
+                        p[i] = int8_amax_pairs(__ldg(src[i] + 2 * u), int8_amax_pairs(__ldg(src[i] + 2 * u + 1), p[i]));
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int r = warp - 2 + 4 * i;
+                const uint32_t m = __reduce_max_sync(0xffffffffu, int8_amax_bits(p[i]));
+                // this slice's magnitude into every CTA's table
+                if (r < nt && lane < S) st_cluster_u32(map_to_cta(smem_u32(&sh.amax[rank][r]), (uint32_t)lane), m);
+            }
+        }
+        cluster_sync();
+        if (wt >= 0) {
+            for (int i = 0; i < kRows; ++i) {
+                const int r = warp - 2 + 4 * i;
+                if (r >= nt) break;
+                uint32_t m = 0u;
+                for (int c = 0; c < S; ++c) m = max(m, sh.amax[c][r]);
+                const Int8Row row = int8_row(__uint_as_float(m));
+                const uint4* x = a.x + (size_t)(m0 + r) * a.ld_x + (size_t)k0 * 16;
+                uint8_t* dst = sB + r * 128;
+                for (int u = lane; u < units; u += 32) {
+                    const uint2 lo = int8_codes8(__ldg(x + 2 * u), row), hi = int8_codes8(__ldg(x + 2 * u + 1), row);
+                    // the 128-byte swizzle: 16-byte chunk c of row r lies at c ^ (r % 8)
+                    *reinterpret_cast<uint4*>(dst + (u >> 3) * C::kBSlot + (((u & 7) ^ (r & 7)) << 4)) =
+                        make_uint4(lo.x, lo.y, hi.x, hi.y);
+                }
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            mbar_arrive(&sh.b_ready);
+        }
+    }
+
+    if (warp == 0) {
+        if (lane == 0) {
+            for (int i = issued; i < steps && ok; ++i) {
+                ok = mbar_wait_bounded(&sh.empty[i % kStages], ((i / kStages) & 1) ^ 1, abort_flag, a.wait_limit_ns);
+                if (ok) request(i, true, true);
+            }
+            if (!ok) {
+                timed_out();
+                for (int s = 0; s < kStages; ++s)  // copies already issued land before shared memory goes away
+                    if (last_phase[s] >= 0) {
+                        volatile int never = 0;
+                        (void)mbar_wait_bounded(&sh.full[s], (uint32_t)last_phase[s], &never, 100000000ull);
+                    }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint64_t a0 = sdesc_kmajor_sw128(smem_u32(sA)), b0 = sdesc_kmajor_sw128(smem_u32(sB));
+            const uint32_t idesc = idesc_i8_cta(N);
+            if (kFused) ok = mbar_wait_bounded(&sh.b_ready, 0, abort_flag, a.wait_limit_ns);
+            for (int i = 0; i < steps && ok; ++i) {
+                const int s = i % kStages;
+                ok = mbar_wait_bounded(&sh.full[s], (i / kStages) & 1, abort_flag, a.wait_limit_ns);
+                if (!ok) break;
+                tc_fence_after_sync();
+                const uint64_t da = a0 + (uint64_t)(s * (kAAtom >> 4));
+                const uint64_t db = b0 + (uint64_t)((kFused ? i : s) * (C::kBSlot >> 4));
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)  // 32 elements of K each
+                    mma_i8_cta(tmem_base, da + kk * 2, db + kk * 2, idesc, (i | kk) != 0 ? 1u : 0u);
+                mma_commit(&sh.empty[s]);
+            }
+            if (!ok) timed_out();
+            mma_commit(&sh.acc_full);
+        }
+        __syncwarp();
+    } else {
+        // ---------------- drain: lanes are channels, TMEM columns tokens
+        const int quad = warp & 3, ch = quad * 32 + lane;
+        const bool got = __all_sync(0xffffffffu,
+                                    mbar_wait_bounded(&sh.acc_full, 0, abort_flag, a.wait_limit_ns));
+        if (!got && lane == 0) timed_out();
+        if (got) {
+            tc_fence_after_sync();
+            for (int c = 0; c < N; c += 16) {
+                uint32_t v[16];
+                tmem_ld_x16(tmem_base + ((uint32_t)(quad * 32) << 16) + c, v);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    if (c + j < nt) s_part[(c + j) * 128 + ch] = (int)v[j];
+            }
+            tc_fence_before_sync();
+        }
+    }
+    cluster_sync();  // every CTA's partial sums are in its shared memory
+    if (wt >= 0) {
+        const int col = n0 + wt;
+        const bool in = col < a.cols_out;
+        const float ws = in ? __ldg(a.w_scales + col) : 0.0f;
+        const uint32_t part = smem_u32(s_part + wt);
+        for (int r = rank; r < nt; r += S) {
+            int sum = 0;
+            for (int c = 0; c < S; ++c) sum += (int)ld_cluster_u32(map_to_cta(part + r * 512, (uint32_t)c));
+            float xs;
+            if (kFused) {
+                uint32_t m = 0u;
+                for (int c = 0; c < S; ++c) m = max(m, sh.amax[c][r]);
+                xs = int8_scale(__uint_as_float(m));
+            } else {
+                xs = __ldg(a.x_scales + m0 + r);
+            }
+            const float y = __int2float_rn(sum) * xs * ws;
+            if (!in) continue;
+            const size_t at = (size_t)(m0 + r) * (size_t)a.ld_out + col;
+            if (a.out_bf16 != 0)
+                reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
+            else
+                reinterpret_cast<float*>(a.out)[at] = y;
+        }
+    }
+    cluster_sync();  // no CTA leaves while another reads its sums
+    if (warp == 1) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem_base, 64);
+    }
+}
+
+template <bool kFused>
+cudaError_t launch_few(const CUtensorMap& ta, const BoxMaps8& tb, FewArgs a, int row_tiles, cudaStream_t s) {
+    constexpr int kDevices = 64;
+    static bool configured[kDevices];
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= kDevices) return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        err = cudaFuncSetAttribute(gemm_int8_few_kernel<kFused>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   (int)FewCfg<kFused>::kSmem);
+        if (err != cudaSuccess) return err;
+        configured[dev] = true;
+    }
+    const int col_tiles = (a.cols_out + 127) / 128;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)a.split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(col_tiles * a.split), (unsigned)row_tiles);
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = FewCfg<kFused>::kSmem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    err = cudaLaunchKernelEx(&cfg, gemm_int8_few_kernel<kFused>, ta, tb, a);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
+// CTAs of a cluster: as many as two CTAs an SM allow for all tiles, each with an atom of K.
+int split_for(long long tiles, int atoms) {
+    int s = 1;
+    while (s < kMaxCluster && tiles * s * 2 <= 2ll * num_sms() && s * 2 <= atoms) s *= 2;
+    return s;
+}
+
+}  // namespace
+
+bool int8_few_fused_fits(long long rows, int cols_in, int cols_out) {
+    if (rows > kFusedTokens) return false;
+    const int atoms = (cols_in + kAtomK8 - 1) / kAtomK8;
+    const int s = split_for((cols_out + 127) / 128, atoms);
+    return (atoms + s - 1) / s <= kFusedAtoms;
+}
+
+cudaError_t launch_int8_few_fused(const CUtensorMap& ta, const __nv_bfloat16* x, long long ld_x, const Int8Gemm& g,
+                                  int cols_in, cudaStream_t s) {
+    FewArgs a{};
+    a.x = reinterpret_cast<const uint4*>(x);
+    a.ld_x = ld_x / 8;
+    a.w_scales = g.w_scale;
+    a.out = g.out;
+    a.ld_out = g.out_ld;
+    a.cols_in = cols_in;
+    a.cols_out = g.out_cols;
+    a.rows = g.rows;
+    a.live = g.live;
+    a.out_bf16 = g.out_bf16;
+    a.split = split_for((g.out_cols + 127) / 128, (cols_in + kAtomK8 - 1) / kAtomK8);
+    a.status = g.status_flags;
+    a.wait_limit_ns = g.wait_limit_ns;
+    return launch_few<true>(ta, BoxMaps8{}, a, 1, s);
+}
+
+cudaError_t launch_int8_few(const CUtensorMap& ta, const BoxMaps8& tb, const Int8Gemm& g, int cols_in, cudaStream_t s) {
+    FewArgs a{};
+    a.x_scales = g.row_scale;
+    a.w_scales = g.w_scale;
+    a.out = g.out;
+    a.ld_out = g.out_ld;
+    a.cols_in = cols_in;
+    a.cols_out = g.out_cols;
+    a.rows = g.rows;
+    a.live = g.live;
+    a.out_bf16 = g.out_bf16;
+    a.early = g.early;
+    a.status = g.status_flags;
+    a.wait_limit_ns = g.wait_limit_ns;
+    const int row_tiles = (g.rows + kFewTokens - 1) / kFewTokens;
+    a.split = split_for((long long)((g.out_cols + 127) / 128) * row_tiles, (cols_in + kAtomK8 - 1) / kAtomK8);
+    return launch_few<false>(ta, tb, a, row_tiles, s);
+}
+
+}  // namespace moe

@@ -222,24 +222,8 @@ moe_status check_product(long long rows, int cols_in, const void* w, const float
     return MOE_OK;
 }
 
-moe_status run_dense(const int8_t* x, const float* x_scales, long long rows, int cols_in, long long ld_x,
-                     const int8_t* w, const float* w_scales, int cols_out, void* out, long long ld_out, int out_bf16,
-                     const int* live, unsigned* status, bool early, cudaStream_t s) {
-    CUtensorMap tA;
-    BoxMaps8 tB;
-    // rows of K bytes; columns past K and rows past the last read as zero
-    const unsigned long long dW[2] = {(unsigned long long)cols_in, (unsigned long long)cols_out};
-    const unsigned long long sW[1] = {(unsigned long long)cols_in};
-    const unsigned long long dX[2] = {(unsigned long long)cols_in, (unsigned long long)rows};
-    const unsigned long long sX[1] = {(unsigned long long)ld_x};
-    const unsigned boxW[2] = {128, 128};
-    if (!make_tensor_map(&tA, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, w, dW, sW, boxW, CU_TENSOR_MAP_SWIZZLE_128B))
-        return MOE_ERR_CUDA;
-    for (int i = 0; i < 8; ++i) {
-        const unsigned box[2] = {128, 16u * (unsigned)(i + 1)};
-        if (!make_tensor_map(&tB.m[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, x, dX, sX, box, CU_TENSOR_MAP_SWIZZLE_128B))
-            return MOE_ERR_CUDA;
-    }
+Int8Gemm dense_params(long long rows, int cols_in, const float* x_scales, const float* w_scales, int cols_out,
+                      void* out, long long ld_out, int out_bf16, const int* live, unsigned* status) {
     Int8Gemm g{};
     g.status_flags = status;
     g.out = out;
@@ -253,9 +237,36 @@ moe_status run_dense(const int8_t* x, const float* x_scales, long long rows, int
     g.live = live;
     g.rows = (int)rows;
     g.out_bf16 = out_bf16;
-    g.early = early;
-    const long long tiles = (rows + kRouteTile - 1) / kRouteTile * g.n_tiles;
-    return launch_gemm_dense_int8(tA, tB, g, tiles, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    return g;
+}
+
+// Rows of K bytes; columns past K and rows past the last read as zero.
+bool row_map(CUtensorMap* map, const void* base, long long rows, int cols, long long ld, unsigned box_rows) {
+    const unsigned long long dims[2] = {(unsigned long long)cols, (unsigned long long)rows};
+    const unsigned long long pitch[1] = {(unsigned long long)ld};
+    const unsigned box[2] = {128, box_rows};
+    return make_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, pitch, box, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+moe_status run_dense(const Int8Gemm& g, const int8_t* x, int cols_in, long long ld_x, const int8_t* w,
+                     cudaStream_t s) {
+    CUtensorMap tA;
+    BoxMaps8 tB;
+    if (!row_map(&tA, w, g.out_cols, cols_in, cols_in, 128)) return MOE_ERR_CUDA;
+    const long long tiles = ((long long)g.rows + kRouteTile - 1) / kRouteTile * g.n_tiles;
+    // Fewer 256 x 256 tiles than a quarter of the SMs' pairs can fill: tiles of 128 x 64 with K split.
+    const bool few = tiles * 4 <= num_sms();
+    // the heights that tiles of these rows can have: any with a live count, else a full and a last one
+    for (int i = 0; i < 8; ++i) {
+        const int h = few ? 16 * (i + 1) : 32 * (i + 1);
+        if (few && i >= 4) break;
+        const int top = few ? 64 : kRouteTile, last = (int)(g.rows % top), step = few ? 16 : 32;
+        const bool used = g.live != nullptr || (g.rows >= top && h == top) ||
+                          (last != 0 && h == (last + step - 1) / step * step);
+        if (used && !row_map(&tB.m[i], x, g.rows, cols_in, ld_x, 16u * (unsigned)(i + 1))) return MOE_ERR_CUDA;
+    }
+    const cudaError_t e = few ? launch_int8_few(tA, tB, g, cols_in, s) : launch_gemm_dense_int8(tA, tB, g, tiles, s);
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 size_t linear_scales_offset(long long rows, int cols_in) {
@@ -357,8 +368,9 @@ moe_status int8_matmul(const int8_t* x, const float* x_scales, long long rows, i
     if (ld_x % 16 != 0 || !is_aligned(x, 16) || !is_aligned(x_scales, 4) || !is_aligned(out, out_bf16 ? 2 : 4))
         return MOE_ERR_ALIGNMENT;
     if (rows == 0) return MOE_OK;
-    return run_dense(x, x_scales, rows, cols_in, ld_x, w, w_scales, cols_out, out, ld_out, out_bf16, live_rows_dev,
-                     status_dev, false, static_cast<cudaStream_t>(stream));
+    const Int8Gemm g = dense_params(rows, cols_in, x_scales, w_scales, cols_out, out, ld_out, out_bf16, live_rows_dev,
+                                    status_dev);
+    return run_dense(g, x, cols_in, ld_x, w, static_cast<cudaStream_t>(stream));
 }
 
 size_t int8_linear_workspace_bytes(long long rows, int cols_in) {
@@ -380,11 +392,18 @@ moe_status int8_linear(const void* x, long long rows, int cols_in, long long ld_
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int8_t* q = static_cast<int8_t*>(workspace);
     float* scales = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + linear_scales_offset(rows, cols_in));
-    if (launch_int8_quantize_rows(static_cast<const __nv_bfloat16*>(x), rows, cols_in, ld_x, q, scales, live_rows_dev,
-                                  s) != cudaSuccess)
+    Int8Gemm g = dense_params(rows, cols_in, scales, w_scales, cols_out, out, ld_out, out_bf16, live_rows_dev,
+                              status_dev);
+    const __nv_bfloat16* rows_in = static_cast<const __nv_bfloat16*>(x);
+    if (int8_few_fused_fits(rows, cols_in, cols_out)) {
+        CUtensorMap tA;
+        if (!row_map(&tA, w, cols_out, cols_in, cols_in, 128)) return MOE_ERR_CUDA;
+        return launch_int8_few_fused(tA, rows_in, ld_x, g, cols_in, s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
+    if (launch_int8_quantize_rows(rows_in, rows, cols_in, ld_x, q, scales, live_rows_dev, s) != cudaSuccess)
         return MOE_ERR_CUDA;
-    return run_dense(q, scales, rows, cols_in, cols_in, w, w_scales, cols_out, out, ld_out, out_bf16, live_rows_dev,
-                     status_dev, true, s);
+    g.early = 1;  // the quantiser releases the product after its own wait
+    return run_dense(g, q, cols_in, cols_in, w, s);
 }
 
 }  // extern "C"

@@ -196,8 +196,10 @@ def test_rows_do_not_depend_on_the_batch():
         _same(part, whole[:n])
 
 
-@pytest.mark.parametrize("rows,K,N,pad", [(1, 64, 40, 0), (1, 2048, 512, 0), (5, 144, 100, 8), (300, 1040, 777, 24),
-                                          (33, 4096, 96, 0)])
+@pytest.mark.parametrize("rows,K,N,pad", [(1, 64, 40, 0), (1, 16, 1, 0), (1, 2048, 512, 0), (1, 8192, 4096, 0), (1, 2688, 40000, 0),
+                                          (5, 144, 100, 8), (16, 16384, 256, 0), (16, 4112, 333, 16), (13, 2048, 8192, 0),
+                                          (17, 2048, 128, 0), (1, 32768, 64, 0), (4, 32768, 40000, 0),
+                                          (300, 1040, 777, 24), (33, 4096, 96, 0), (64, 1024, 8000, 0), (65, 1024, 8000, 0)])
 def test_linear_is_the_two_calls(rows, K, N, pad):
     g = torch.Generator().manual_seed(rows + K)
     x = torch.randn((rows, K + pad), generator=g).to(torch.bfloat16)
@@ -234,6 +236,25 @@ def test_linear_in_a_graph_with_live_counts():
         want = torch.full((rows, N), -5.0)
         q, s = quantize_ref(xc)
         want[:n] = product_ref(q[:n], s[:n], wc, sc, False)
+        _same(out, want)
+
+
+@pytest.mark.parametrize("live", [0, 1, 3, 16, 40, -2])
+def test_few_tokens_with_a_live_count(live):
+    """Buffers of 16 rows (quantised in the product's launch) and of 40, rows past the live count untouched."""
+    g = torch.Generator().manual_seed(14)
+    for rows, K, N in ((16, 1040, 200), (40, 1040, 200)):
+        n = max(0, min(live, rows))
+        x = torch.randn((rows, K), generator=g).to(torch.bfloat16)
+        x[n:] = float("nan")
+        wq, ws = _codes((N, K), g), _scales(N, g)
+        out = torch.full((rows, N + 1), -5.0, device="cuda")
+        buf = torch.empty(rm.int8_linear_workspace_bytes(rows, K), dtype=torch.uint8, device="cuda")
+        rm.int8_linear(x.cuda(), wq.cuda(), ws.cuda(), out[:, :N], buf,
+                       live_rows=torch.tensor([live], dtype=torch.int32, device="cuda"))
+        want = torch.full((rows, N + 1), -5.0)
+        if n:
+            want[:n, :N] = product_ref(*quantize_ref(x[:n]), wq, ws, False)
         _same(out, want)
 
 
