@@ -10,7 +10,7 @@
 //   kFused   up to 16 tokens of bf16: each CTA quantises its own slice of the
 //            rows into the swizzled operand layout in shared memory; the rows'
 //            largest magnitudes meet in one cluster barrier.  One launch does all.
-//   !kFused  up to 64 tokens a tile, whose codes TMA loads beside the weights.
+//   !kFused  up to 128 tokens a tile, whose codes TMA loads beside the weights.
 //
 // Roles (6 warps): warp 0 issues TMA loads, warp 1 owns TMEM and issues the MMAs
 // (tcgen05 kind::i8, M = 128), warps 2-5 quantise (kFused) and drain.  Every
@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kFewThreads = 192;
 constexpr int kWorkers = 128;              // warps 2..5
-constexpr int kFewTokens = 64;             // tokens of a tile at most
+constexpr int kFewTokens = 128;            // tokens of a tile at most
 constexpr int kFusedTokens = 16;
 constexpr int kFusedAtoms = 16;            // 128-element atoms of a K slice that kFused holds
 constexpr uint32_t kAAtom = 128 * 128;     // 128 weight rows of 128 bytes
@@ -32,11 +32,15 @@ constexpr int kMaxCluster = 8;
 
 template <bool kFused>
 struct FewCfg {
+    static constexpr int kTokens = kFused ? kFusedTokens : kFewTokens;
     static constexpr int kStages = kFused ? 4 : 3;
-    static constexpr uint32_t kBSlot = kFused ? kFusedTokens * 128 : kFewTokens * 128;  // an atom of the tokens
+    static constexpr uint32_t kBSlot = kTokens * 128;  // an atom of the tokens
     static constexpr uint32_t kBBytes = kBSlot * (kFused ? kFusedAtoms : kStages);
-    static constexpr uint32_t kPartBytes = (kFused ? kFusedTokens : kFewTokens) * 128 * 4;
-    static constexpr size_t kSmem = 1024 + kStages * kAAtom + kBBytes + kPartBytes + 512;
+    static constexpr uint32_t kPartBytes = kTokens * 128 * 4;  // takes the weight stages' place after the MMAs
+    static constexpr uint32_t kOperands = kStages * kAAtom + kBBytes;
+    static constexpr uint32_t kTmemCols = kFused ? 32 : 128;
+    static constexpr size_t kSmem = 1024 + kOperands;
+    static_assert(kPartBytes <= kOperands, "the partial sums take the operands' place");
 };
 
 struct __align__(8) FewShared {
@@ -88,9 +92,12 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr) {
-    uint32_t v;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+__device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr) {
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
     return v;
 }
 __device__ __forceinline__ void st_cluster_u32(uint32_t addr, uint32_t v) {
@@ -112,7 +119,7 @@ __global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sA = smem;
     uint8_t* sB = sA + kStages * kAAtom;
-    int* s_part = reinterpret_cast<int*>(sB + C::kBBytes);  // [token][128 channels]
+    int* s_part = reinterpret_cast<int*>(smem);  // [token][128 channels], once every operand has been read
     volatile int* abort_flag = &sh.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int S = a.split, rank = (int)cluster_ctarank();
@@ -134,7 +141,7 @@ __global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid
         fence_barrier_init();
     }
     if (warp == 1) {
-        tmem_alloc(&sh.tmem_base, 64);
+        tmem_alloc(&sh.tmem_base, C::kTmemCols);
         tmem_relinquish();
     }
     tc_fence_before_sync();
@@ -150,7 +157,7 @@ __global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid
     if (nt <= 0) {                              // the whole cluster: same tile
         if (a.early) pdl_wait();
         __syncthreads();
-        if (warp == 1) tmem_dealloc(tmem_base, 64);
+        if (warp == 1) tmem_dealloc(tmem_base, C::kTmemCols);
         return;
     }
     const int N = (nt + 15) & ~15;
@@ -160,6 +167,7 @@ __global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid
         if (a.status != nullptr) atomicOr(a.status, MOE_DEV_TIMEOUT);
     };
 
+    float ws[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     int issued = 0, last_phase[4] = {-1, -1, -1, -1};
     bool ok = true;
     // step i of the slice into its stage: weights, and the tokens' codes (!kFused)
@@ -217,7 +225,8 @@ __global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid
                 const int r = warp - 2 + 4 * i;
                 if (r >= nt) break;
                 uint32_t m = 0u;
-                for (int c = 0; c < S; ++c) m = max(m, sh.amax[c][r]);
+#pragma unroll
+                for (int c = 0; c < kMaxCluster; ++c) m = c < S ? max(m, sh.amax[c][r]) : m;
                 const Int8Row row = int8_row(__uint_as_float(m));
                 const uint4* x = a.x + (size_t)(m0 + r) * a.ld_x + (size_t)k0 * 16;
                 uint8_t* dst = sB + r * 128;
@@ -273,6 +282,10 @@ __global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid
     } else {
         // ---------------- drain: lanes are channels, TMEM columns tokens
         const int quad = warp & 3, ch = quad * 32 + lane;
+        // the scales of this lane's four columns in the last step, meanwhile
+        const int left = a.cols_out - n0 - lane * 4;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ws[q] = q < left ? __ldg(a.w_scales + n0 + lane * 4 + q) : 0.0f;
         const bool got = __all_sync(0xffffffffu,
                                     mbar_wait_bounded(&sh.acc_full, 0, abort_flag, a.wait_limit_ns));
         if (!got && lane == 0) timed_out();
@@ -291,34 +304,65 @@ __global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid
     }
     cluster_sync();  // every CTA's partial sums are in its shared memory
     if (wt >= 0) {
-        const int col = n0 + wt;
-        const bool in = col < a.cols_out;
-        const float ws = in ? __ldg(a.w_scales + col) : 0.0f;
-        const uint32_t part = smem_u32(s_part + wt);
-        for (int r = rank; r < nt; r += S) {
-            int sum = 0;
-            for (int c = 0; c < S; ++c) sum += (int)ld_cluster_u32(map_to_cta(part + r * 512, (uint32_t)c));
+        // a warp takes a token, a lane four channels: rows rank + S * (w, w + 4, ...)
+        const int col = n0 + lane * 4, left = a.cols_out - col;  // columns of this lane inside out (may be <= 0)
+        // whole stores of the lane's four columns: all inside, rows and base aligned for them
+        const bool wide = left >= 4 && a.ld_out % 4 == 0 &&
+                          (reinterpret_cast<uintptr_t>(a.out) & (a.out_bf16 != 0 ? 7 : 15)) == 0;
+        const uint32_t part = smem_u32(s_part) + (uint32_t)lane * 16u;
+#pragma unroll 1
+        for (int r = rank + S * (warp - 2); r < nt; r += 4 * S) {
+            int4 v[kMaxCluster];  // all on their way before the first is added
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c)
+                v[c] = c < S ? ld_cluster_v4(map_to_cta(part + (uint32_t)r * 512u, (uint32_t)c)) : make_int4(0, 0, 0, 0);
+            int4 sum = v[0];
+#pragma unroll
+            for (int c = 1; c < kMaxCluster; ++c) {
+                sum.x += v[c].x;
+                sum.y += v[c].y;
+                sum.z += v[c].z;
+                sum.w += v[c].w;
+            }
             float xs;
             if (kFused) {
                 uint32_t m = 0u;
-                for (int c = 0; c < S; ++c) m = max(m, sh.amax[c][r]);
+#pragma unroll
+                for (int c = 0; c < kMaxCluster; ++c) m = c < S ? max(m, sh.amax[c][r]) : m;
                 xs = int8_scale(__uint_as_float(m));
             } else {
                 xs = __ldg(a.x_scales + m0 + r);
             }
-            const float y = __int2float_rn(sum) * xs * ws;
-            if (!in) continue;
+            const float y[4] = {__int2float_rn(sum.x) * xs * ws[0], __int2float_rn(sum.y) * xs * ws[1],
+                                __int2float_rn(sum.z) * xs * ws[2], __int2float_rn(sum.w) * xs * ws[3]};
             const size_t at = (size_t)(m0 + r) * (size_t)a.ld_out + col;
-            if (a.out_bf16 != 0)
-                reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(y);
-            else
-                reinterpret_cast<float*>(a.out)[at] = y;
+            if (a.out_bf16 != 0) {
+                __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(a.out) + at;
+                if (wide) {
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(y[0], y[1]), hi = __floats2bfloat162_rn(y[2], y[3]);
+                    *reinterpret_cast<uint2*>(dst) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                                *reinterpret_cast<const uint32_t*>(&hi));
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (q < left) dst[q] = __float2bfloat16_rn(y[q]);
+                }
+            } else {
+                float* dst = reinterpret_cast<float*>(a.out) + at;
+                if (wide) {
+                    *reinterpret_cast<float4*>(dst) = make_float4(y[0], y[1], y[2], y[3]);
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (q < left) dst[q] = y[q];
+                }
+            }
         }
     }
     cluster_sync();  // no CTA leaves while another reads its sums
     if (warp == 1) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem_base, 64);
+        tmem_dealloc(tmem_base, C::kTmemCols);
     }
 }
 
@@ -354,19 +398,23 @@ cudaError_t launch_few(const CUtensorMap& ta, const BoxMaps8& tb, FewArgs a, int
     return err != cudaSuccess ? err : cudaGetLastError();
 }
 
-// CTAs of a cluster: as many as two CTAs an SM allow for all tiles, each with an atom of K.
-int split_for(long long tiles, int atoms) {
+}  // namespace
+
+// CTAs of a cluster: as many as fill the SMs once, or twice where each keeps four atoms of K (one
+// token, 2048 -> 4096: 5.9 us with four CTAs of four atoms, 6.6 us with eight of two; 16 tokens,
+// 8192 -> 4096: 9.5 us with eight of eight, 11.4 us with four of sixteen).
+int int8_split_for(long long tiles, int atoms) {
     int s = 1;
-    while (s < kMaxCluster && tiles * s * 2 <= 2ll * num_sms() && s * 2 <= atoms) s *= 2;
+    while (s < kMaxCluster && atoms >= 2 * s &&
+           (tiles * s * 2 <= num_sms() || (tiles * s <= num_sms() && atoms >= 8 * s)))
+        s *= 2;
     return s;
 }
-
-}  // namespace
 
 bool int8_few_fused_fits(long long rows, int cols_in, int cols_out) {
     if (rows > kFusedTokens) return false;
     const int atoms = (cols_in + kAtomK8 - 1) / kAtomK8;
-    const int s = split_for((cols_out + 127) / 128, atoms);
+    const int s = int8_split_for((cols_out + 127) / 128, atoms);
     return (atoms + s - 1) / s <= kFusedAtoms;
 }
 
@@ -383,7 +431,7 @@ cudaError_t launch_int8_few_fused(const CUtensorMap& ta, const __nv_bfloat16* x,
     a.rows = g.rows;
     a.live = g.live;
     a.out_bf16 = g.out_bf16;
-    a.split = split_for((g.out_cols + 127) / 128, (cols_in + kAtomK8 - 1) / kAtomK8);
+    a.split = int8_split_for((g.out_cols + 127) / 128, (cols_in + kAtomK8 - 1) / kAtomK8);
     a.status = g.status_flags;
     a.wait_limit_ns = g.wait_limit_ns;
     return launch_few<true>(ta, BoxMaps8{}, a, 1, s);
@@ -404,7 +452,7 @@ cudaError_t launch_int8_few(const CUtensorMap& ta, const BoxMaps8& tb, const Int
     a.status = g.status_flags;
     a.wait_limit_ns = g.wait_limit_ns;
     const int row_tiles = (g.rows + kFewTokens - 1) / kFewTokens;
-    a.split = split_for((long long)((g.out_cols + 127) / 128) * row_tiles, (cols_in + kAtomK8 - 1) / kAtomK8);
+    a.split = int8_split_for((long long)((g.out_cols + 127) / 128) * row_tiles, (cols_in + kAtomK8 - 1) / kAtomK8);
     return launch_few<false>(ta, tb, a, row_tiles, s);
 }
 

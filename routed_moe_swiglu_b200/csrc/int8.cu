@@ -248,19 +248,37 @@ bool row_map(CUtensorMap* map, const void* base, long long rows, int cols, long 
     return make_tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, base, dims, pitch, box, CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
+// Whether 128 x 128 tiles with K split over clusters (gemm_int8_few.cu) beat 256 x 256 tiles of CTA
+// pairs.  Both are bound by what an SM takes in, and the split one pays for draining and adding
+// partial sums.  Estimates in us, fitted to 105 sizes (K 1024..8192, N 512..16384, 16..1024
+// tokens); at K 8192, N 4096: 64 tokens 11.6 split against 18.0, 256 tokens 17.4 against 24.5,
+// 1024 tokens 38.8 against 26.1.
+bool few_is_faster(const Int8Gemm& g, int cols_in) {
+    const double sms = num_sms(), K = cols_in;
+    const long long rows = g.rows;
+    const double wide_n = rows < kRouteTile ? (double)((rows + 31) / 32 * 32) : (double)kRouteTile;
+    const long long wide = (rows + kRouteTile - 1) / kRouteTile * g.n_tiles;
+    const double waves = (double)((wide + (long long)(sms / 2) - 1) / (long long)(sms / 2));
+    const double t_wide = 3.0 + (rows > 128 ? 2.2 : 0.0) + waves * K * (128.0 + wide_n / 2) / 88e3;
+    const double few_n = rows < 128 ? (double)((rows + 15) / 16 * 16) : 128.0;
+    const long long tiles = (rows + 127) / 128 * ((g.out_cols + 127) / 128);
+    const int split = int8_split_for(tiles, g.atoms);
+    const double per_sm = (double)((tiles * split + (long long)sms - 1) / (long long)sms);  // CTAs
+    const double t_few = 3.3 + 3.6 * few_n / 128 + per_sm * K / split * (128.0 + few_n) / 70e3;
+    return t_few < t_wide;
+}
+
 moe_status run_dense(const Int8Gemm& g, const int8_t* x, int cols_in, long long ld_x, const int8_t* w,
                      cudaStream_t s) {
     CUtensorMap tA;
     BoxMaps8 tB;
     if (!row_map(&tA, w, g.out_cols, cols_in, cols_in, 128)) return MOE_ERR_CUDA;
     const long long tiles = ((long long)g.rows + kRouteTile - 1) / kRouteTile * g.n_tiles;
-    // Fewer 256 x 256 tiles than a quarter of the SMs' pairs can fill: tiles of 128 x 64 with K split.
-    const bool few = tiles * 4 <= num_sms();
+    const bool few = few_is_faster(g, cols_in);
     // the heights that tiles of these rows can have: any with a live count, else a full and a last one
     for (int i = 0; i < 8; ++i) {
         const int h = few ? 16 * (i + 1) : 32 * (i + 1);
-        if (few && i >= 4) break;
-        const int top = few ? 64 : kRouteTile, last = (int)(g.rows % top), step = few ? 16 : 32;
+        const int top = few ? 128 : kRouteTile, last = (int)(g.rows % top), step = few ? 16 : 32;
         const bool used = g.live != nullptr || (g.rows >= top && h == top) ||
                           (last != 0 && h == (last + step - 1) / step * step);
         if (used && !row_map(&tB.m[i], x, g.rows, cols_in, ld_x, 16u * (unsigned)(i + 1))) return MOE_ERR_CUDA;

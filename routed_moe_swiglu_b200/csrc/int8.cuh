@@ -123,6 +123,7 @@ cudaError_t launch_gemm2_int8(const CUtensorMap& a, const BoxMaps8& b, const Int
 cudaError_t launch_gemm_dense_int8(const CUtensorMap& a, const BoxMaps8& b, const Int8Gemm& g, long long max_tiles,
                                    cudaStream_t s);
 // Few tokens (gemm_int8_few.cu): bf16 rows quantised in the same launch, where they fit, or codes.
+int int8_split_for(long long tiles, int atoms);  // CTAs that share a tile's K
 bool int8_few_fused_fits(long long rows, int cols_in, int cols_out);
 cudaError_t launch_int8_few_fused(const CUtensorMap& a, const __nv_bfloat16* x, long long ld_x, const Int8Gemm& g,
                                   int cols_in, cudaStream_t s);
