@@ -392,8 +392,10 @@ def _dense(name: str, t, dtype, shape) -> None:
 
 def _rows(name: str, t, dtype, rows: int, cols: int) -> None:
     """`t` (or None) must be a dense matrix of this dtype with `cols` columns and at least `rows` rows."""
-    if t is not None and (t.dtype is not dtype or t.dim() != 2 or t.shape[0] < rows or t.shape[1] != cols
-                          or not t.is_contiguous()):
+    if t is None:
+        return
+    shape = t.shape
+    if t.dtype is not dtype or len(shape) != 2 or shape[0] < rows or shape[1] != cols or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} matrix of {cols} columns and at least {rows} rows, not "
                          f"{t.dtype} {tuple(t.shape)} with strides {t.stride()}")
 

@@ -545,12 +545,24 @@ __global__ void __launch_bounds__(kGradThreads) route_backward_kernel(const Rout
                     if (v * L + gl < E) s_row[v * L + gl] = x[v];
             }
             __syncwarp();
+            // routes of different experts add in any order; an expert named twice, or more routes
+            // than lanes: one route after another
+            bool apart = k <= L;
+            if (apart) {
+                const unsigned key = id[0] >= 0 ? (unsigned)(id[0] * kGroups + lane / L) : 0x80000000u + lane;
+                apart = __all_sync(0xffffffffu, __popc(__match_any_sync(0xffffffffu, key)) == 1);
+            }
+            if (apart) {
+                if (id[0] >= 0) s_row[id[0]] += w[0] * (d[0] - wd);
+                __syncwarp();
+            } else {
 #pragma unroll
-            for (int r = 0; r < kSlots; ++r)
-                for (int j = r * L; j < min(k, r * L + L); ++j) {
-                    if (gl == j - r * L && id[r] >= 0) s_row[id[r]] += w[r] * (d[r] - wd);
-                    __syncwarp();
-                }
+                for (int r = 0; r < kSlots; ++r)
+                    for (int j = r * L; j < min(k, r * L + L); ++j) {
+                        if (gl == j - r * L && id[r] >= 0) s_row[id[r]] += w[r] * (d[r] - wd);
+                        __syncwarp();
+                    }
+            }
             if (kVec) {
 #pragma unroll
                 for (int q = 0; q < V / 4; ++q) {
