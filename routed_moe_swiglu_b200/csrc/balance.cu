@@ -22,9 +22,11 @@
 // registers: the softmax is one pass over the logits.  A block takes a
 // contiguous run of tokens and walks the sequences it meets; each (block b,
 // sequence s) pair it meets writes its sums to slot b + s.  Blocks and
-// sequences both advance along the tokens, so no two pairs share a slot, and
-// the second kernel adds a sequence's slots in block order: no float atomics,
-// the same bits every run.
+// sequences both advance along the tokens, so no two pairs share a slot, and a
+// finishing step adds a sequence's slots in block order: no float atomics, the
+// same bits every run.  Long runs of a sequence are shared by the block's warps;
+// runs of a few tokens are a warp's own.  The rows come through a ring in shared
+// memory that each lane fills for itself (cp.async), two rows ahead.
 #include <cmath>
 
 #include "moe_internal.cuh"
@@ -36,11 +38,19 @@ namespace {
 constexpr int kBalThreads = 512;
 constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalSumRows = kBalWarps / 2;  // rows of sums in shared memory: half of the warps add the other half's
+template <int V>
+constexpr int kRingOf = V <= 16 ? 3 : 2;    // rows of a lane group in flight or in use
+constexpr int kShortPasses = 4;             // a sequence's run of so many passes of a warp is that warp's alone
 constexpr int kGradThreads = 256;
 constexpr int kGradWarps = kGradThreads / 32;
+template <int V>
+constexpr int kGradBlocks = V <= 8 ? 4 : V <= 16 ? 3 : 2;  // of an SM: the grid is one wave of them
 constexpr int kFinThreads = 1024;
 constexpr int kFinWarps = kFinThreads / 32;
-constexpr int kFinCols = 32;  // columns of an item of the finish: a warp per slot row, a lane per column
+constexpr int kFinBlocks = 8;               // of the finishing kernel where it is one cluster
+constexpr int kFinGroup = 8;                // its warps that add an item's slots together
+constexpr int kFinCols = 32;                // columns of an item of the finish
+constexpr int kBatch = 8;                   // loads of the finish in flight
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BalanceArgs {
@@ -64,7 +74,7 @@ struct BalanceArgs {
     float* seq_dot;     // [num_seqs][col blocks]
     float* seq_z;       // [num_seqs]
     int* seq_n;         // [num_seqs]
-    unsigned* ticket;
+    unsigned* ticket;   // zeroed by the sums' kernel, counted by the finishing one
 };
 
 __device__ __forceinline__ int seq_begin(const int* off, int s, int n) {
@@ -86,6 +96,22 @@ __device__ __forceinline__ int find_seq(const int* off, int num_seqs, int t) {
     return lo;
 }
 
+// The same for a whole warp that asks for one token.
+__device__ __forceinline__ int find_seq_warp(const int* off, int num_seqs, int t) {
+    if (off == nullptr) return 0;
+    int lo = 0, hi = num_seqs;
+    while (hi - lo > 32) {
+        const int mid = (lo + hi) >> 1;
+        if (__ldg(off + mid + 1) > t)
+            hi = mid;
+        else
+            lo = mid + 1;
+    }
+    const int s = lo + (int)(threadIdx.x & 31);
+    const unsigned past = __ballot_sync(0xffffffffu, s >= hi || __ldg(off + s + 1) > t);
+    return past != 0u ? lo + __ffs(past) - 1 : hi;
+}
+
 template <int L>
 __device__ __forceinline__ float group_max(float v) {
 #pragma unroll
@@ -104,27 +130,77 @@ template <int L, bool kVec>
 __device__ __forceinline__ int col_of(int v, int gl) {
     return kVec ? (v >> 2) * (4 * L) + gl * 4 + (v & 3) : v * L + gl;
 }
-// V values of a row per lane; columns from E on, and all of an absent row, read as `fill`.
+// One row per lane group on its way into the lanes' own places of a ring slot: 16-byte runs, or
+// single floats where rows do not start on 16 bytes.
 template <int L, int V, bool kVec>
-__device__ __forceinline__ void load_row(const float* row, int E, int gl, bool have, float fill, float (&x)[V]) {
+__device__ __forceinline__ void ring_request(float* slot, const float* row, int E, int gl, bool have) {
+    const int lane = threadIdx.x & 31;
+    if (have) {
+        if (kVec) {
+#pragma unroll
+            for (int q = 0; q < V / 4; ++q) {
+                const int c = q * (4 * L) + gl * 4;  // E % 4 == 0: a run is in or out
+                if (c < E)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(slot + (q * 32 + lane) * 4)),
+                                 "l"(row + c)
+                                 : "memory");
+            }
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int c = v * L + gl;
+                if (c < E)
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(slot + v * 32 + lane)),
+                                 "l"(row + c)
+                                 : "memory");
+            }
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int kRing>
+__device__ __forceinline__ void ring_wait() {  // the oldest of kRing - 1 requests is there
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+}
+__device__ __forceinline__ void ring_drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+// The lane's V values of a row; columns from E on, and all of an absent row, read as -infinity.
+template <int L, int V, bool kVec>
+__device__ __forceinline__ void ring_read(const float* slot, int E, int gl, bool have, float (&x)[V]) {
+    const int lane = threadIdx.x & 31;
     if (kVec) {
 #pragma unroll
         for (int q = 0; q < V / 4; ++q) {
-            const int c = q * (4 * L) + gl * 4;  // E % 4 == 0: a run is in or out
-            float4 f = make_float4(fill, fill, fill, fill);
-            if (have && c < E) f = __ldg(reinterpret_cast<const float4*>(row + c));
-            x[4 * q] = f.x;
-            x[4 * q + 1] = f.y;
-            x[4 * q + 2] = f.z;
-            x[4 * q + 3] = f.w;
+            const float4 f = *reinterpret_cast<const float4*>(slot + (q * 32 + lane) * 4);
+            const bool in = have && q * (4 * L) + gl * 4 < E;
+            x[4 * q] = in ? f.x : -INFINITY;
+            x[4 * q + 1] = in ? f.y : -INFINITY;
+            x[4 * q + 2] = in ? f.z : -INFINITY;
+            x[4 * q + 3] = in ? f.w : -INFINITY;
         }
     } else {
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int c = v * L + gl;
-            x[v] = have && c < E ? __ldg(row + c) : fill;
+        for (int v = 0; v < V; ++v) x[v] = have && v * L + gl < E ? slot[v * 32 + lane] : -INFINITY;
+    }
+}
+// Writes the lane's values back to its places.
+template <int V, bool kVec>
+__device__ __forceinline__ void ring_write(float* slot, const float (&x)[V]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (kVec) {
+            if (v % 4 == 0)
+                *reinterpret_cast<float4*>(slot + (v / 4 * 32 + lane) * 4) = make_float4(x[v], x[v + 1], x[v + 2],
+                                                                                       x[v + 3]);
+        } else {
+            slot[v * 32 + lane] = x[v];
         }
     }
+}
+// Where column c of the row of group `group` lies in a slot.
+template <int L, bool kVec>
+__device__ __forceinline__ int ring_place(int c, int group) {
+    return kVec ? ((c / (4 * L)) * 32 + group * L + (c / 4) % L) * 4 + c % 4 : c / L * 32 + group * L + c % L;
 }
 
 __device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; 0 for -infinity
@@ -138,21 +214,95 @@ struct StatsShared {
     int n[kBalWarps];
 };
 struct FinishShared {
-    float p[kFinWarps][kFinCols + 1];
-    int c[kFinWarps][kFinCols + 1];
-    double a[kFinWarps], b[kFinWarps];
+    float p[kFinWarps][kFinCols];
+    int c[kFinWarps][kFinCols];
+    float z[kFinWarps];
+    int n[kFinWarps];
     int i[kFinWarps], j[kFinWarps];
 };
 
-// Sums of this block's tokens, one slot for each sequence it meets.  The next token's row is on
-// its way while this one's softmax is computed.
-template <int L, int V, bool kVec>
-__device__ __forceinline__ void balance_stats(const BalanceArgs& a, int n, float* s_sum, int* s_cnt,
-                                              StatsShared& sh) {
+// Sums over the tokens t, t + step, ... < t_hi of one sequence, t the first of this lane's group
+// and tw the first of the warp's groups: acc += p, z += lse^2, cnt += 1 for each that counts;
+// `count(id)` for each of its routes.
+template <int L, int V, bool kVec, class Count>
+__device__ __forceinline__ void sum_tokens(const BalanceArgs& a, float* ring, int tw, int t_hi, int step,
+                                           float (&acc)[V], float& z, int& cnt, Count count) {
     const int E = a.E, k = a.k;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int gl = lane & (L - 1);
+    const int lane = threadIdx.x & 31, gl = lane & (L - 1);
+    constexpr int kSlot = 32 * V, kRing = kRingOf<V>;
+    int t = tw + lane / L;
+    auto kept = [&](int tt) { return tt < t_hi && (a.mask == nullptr || __ldg(a.mask + tt) != 0); };
+    bool have[kRing];  // of the rows in the ring's slots, the oldest first
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i) {
+        have[i] = kept(t + i * step);
+        ring_request<L, V, kVec>(ring + i * kSlot, a.logits + (size_t)(t + i * step) * E, E, gl, have[i]);
+    }
+    int slot = 0;
+    for (; tw < t_hi; tw += step, t += step) {
+        have[kRing - 1] = kept(t + (kRing - 1) * step);
+        // the routes are on their way before the softmax needs its row
+        int id0 = -1;
+        if (have[0] && gl < k) id0 = __ldg(a.ids + (size_t)t * k + gl);
+        ring_wait<kRing>();
+        float x[V];
+        ring_read<L, V, kVec>(ring + slot * kSlot, E, gl, have[0], x);
+        const int refill = slot + kRing - 1 < kRing ? slot + kRing - 1 : slot - 1;
+        ring_request<L, V, kVec>(ring + refill * kSlot, a.logits + (size_t)(t + (kRing - 1) * step) * E, E, gl,
+                                 have[kRing - 1]);
+        float mx = -INFINITY;
+#pragma unroll
+        for (int v = 0; v < V; ++v) mx = fmaxf(mx, x[v]);
+        mx = group_max<L>(mx);
+        if (mx == -INFINITY) mx = 0.0f;  // all -infinity: the sum below is 0 (NaN with a NaN logit)
+        float sum = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x[v] = exp2_approx((x[v] - mx) * kLog2e);  // the difference first: rows near the type's bounds
+            sum += x[v];
+        }
+        sum = group_sum<L>(sum);
+        const bool counted = have[0] && sum != 0.0f;  // true for NaN: it shows in the losses
+        const float inv = counted ? __frcp_rn(sum) : 0.0f;
+        const float lse = counted ? mx + logf(sum) : -INFINITY;
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] = fmaf(x[v], inv, acc[v]);  // 0 * 0 where it does not count
+        if (t < t_hi && gl == 0) {
+            a.lse[t] = lse;
+            if (counted) {
+                z += lse * lse;
+                ++cnt;
+            }
+        }
+        if (counted) {
+            if (id0 >= 0 && id0 < E) count(id0);
+            for (int j = gl + L; j < k; j += L) {
+                const int id = __ldg(a.ids + (size_t)t * k + j);
+                if (id >= 0 && id < E) count(id);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRing - 1; ++i) have[i] = have[i + 1];
+        slot = slot + 1 == kRing ? 0 : slot + 1;
+    }
+    ring_drain();
+    // the groups of the warp: every lane then holds the warp's sum of its columns
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int o = L; o < 32; o <<= 1) acc[v] += __shfl_xor_sync(0xffffffffu, acc[v], o);
+    z = group_sum<32>(z);
+    cnt = __reduce_add_sync(0xffffffffu, cnt);
+}
+
+// Sums of this block's tokens, one slot for each sequence it meets.
+template <int L, int V, bool kVec>
+__device__ __forceinline__ void balance_stats(const BalanceArgs& a, int n, float* ring, float* s_sum, int* s_cnt,
+                                              StatsShared& sh) {
+    const int E = a.E;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gl = lane & (L - 1);
     constexpr int kGroups = 32 / L;  // tokens a warp holds at once
+    constexpr int kShort = kShortPasses * kGroups;
     const int chunk = (n + a.blocks - 1) / a.blocks;
     const int c0 = min(n, (int)blockIdx.x * chunk), c1 = min(n, c0 + chunk);
     if (c0 >= c1) return;
@@ -161,72 +311,60 @@ __device__ __forceinline__ void balance_stats(const BalanceArgs& a, int n, float
     for (int t = c0 + threadIdx.x; t < c1; t += kBalThreads)
         if (t < first || t >= last) a.lse[t] = -INFINITY;
 
-    for (int s = find_seq(a.seq_off, a.num_seqs, c0); s < a.num_seqs; ++s) {
+    // The runs of this block: of each sequence, [t_lo, t_hi).  First the short ones, a warp each in
+    // turn, then the long ones, all warps together.
+    const int s0 = find_seq_warp(a.seq_off, a.num_seqs, c0);
+    int runs = 0, longs = 0;
+    for (int s = s0; s < a.num_seqs; ++s) {
         const int sb = seq_begin(a.seq_off, s, n);
         if (sb >= c1) break;
         const int t_lo = max(sb, c0), t_hi = min(seq_begin(a.seq_off, s + 1, n), c1);
         if (t_lo >= t_hi) continue;
-        for (int e = threadIdx.x; e < E; e += kBalThreads) s_cnt[e] = 0;
-        __syncthreads();
-        float acc[V], next[V];
+        if (t_hi - t_lo > kShort) {
+            ++longs;
+            continue;
+        }
+        if (runs++ % kBalWarps != warp) continue;
+        const size_t slot = (size_t)blockIdx.x + s;
+        float acc[V], z = 0.0f;
+        int cnt = 0;
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-        float z = 0.0f;
-        int cnt = 0;
-        constexpr int kStep = kBalWarps * kGroups;
-        int t = t_lo + warp * kGroups + lane / L;
-        auto kept = [&](int tt) { return tt < t_hi && (a.mask == nullptr || __ldg(a.mask + tt) != 0); };
-        bool have_next = kept(t);
-        load_row<L, V, kVec>(a.logits + (size_t)t * E, E, gl, have_next, -INFINITY, next);
-        for (int tw = t_lo + warp * kGroups; tw < t_hi; tw += kStep, t += kStep) {
-            const bool have = have_next;
-            float x[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) x[v] = next[v];
-            have_next = kept(t + kStep);
-            load_row<L, V, kVec>(a.logits + (size_t)(t + kStep) * E, E, gl, have_next, -INFINITY, next);
-            float mx = -INFINITY;
-#pragma unroll
-            for (int v = 0; v < V; ++v) mx = fmaxf(mx, x[v]);
-            mx = group_max<L>(mx);
-            if (mx == -INFINITY) mx = 0.0f;  // all -infinity: the sum below is 0 (NaN with a NaN logit)
-            float sum = 0.0f;
+        int* counts = a.slot_c + slot * E;
+        for (int e = lane; e < E; e += 32) counts[e] = 0;
+        __syncwarp();
+        sum_tokens<L, V, kVec>(a, ring, t_lo, t_hi, kGroups, acc, z, cnt, [&](int id) { atomicAdd(counts + id, 1); });
+        if (lane < L)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                x[v] = exp2_approx((x[v] - mx) * kLog2e);  // the difference first: rows near the type's bounds
-                sum += x[v];
+                const int c = col_of<L, kVec>(v, gl);
+                if (c < E) a.slot_p[slot * E + c] = acc[v];
             }
-            sum = group_sum<L>(sum);
-            const bool counted = have && sum != 0.0f;  // true for NaN: it shows in the losses
-            const float inv = counted ? __frcp_rn(sum) : 0.0f;
-            const float lse = counted ? mx + logf(sum) : -INFINITY;
-#pragma unroll
-            for (int v = 0; v < V; ++v) acc[v] = fmaf(x[v], inv, acc[v]);  // 0 * 0 where it does not count
-            if (t < t_hi && gl == 0) {
-                a.lse[t] = lse;
-                if (counted) {
-                    z += lse * lse;
-                    ++cnt;
-                }
-            }
-            if (counted)
-                for (int j = gl; j < k; j += L) {
-                    const int id = __ldg(a.ids + (size_t)t * k + j);
-                    if (id >= 0 && id < E) atomicAdd(&s_cnt[id], 1);  // integers: any order
-                }
+        if (lane == 0) {
+            a.slot_z[slot] = z;
+            a.slot_n[slot] = cnt;
         }
-        // groups of the warp, then warps in order: the upper half's rows first go through shared
-        // memory to the lower half, which adds them and leaves its rows there
+    }
+    if (longs == 0) return;
+    for (int s = s0; s < a.num_seqs; ++s) {
+        const int sb = seq_begin(a.seq_off, s, n);
+        if (sb >= c1) break;
+        const int t_lo = max(sb, c0), t_hi = min(seq_begin(a.seq_off, s + 1, n), c1);
+        if (t_hi - t_lo <= kShort) continue;
+        for (int e = threadIdx.x; e < E; e += kBalThreads) s_cnt[e] = 0;
+        __syncthreads();
+        float acc[V], z = 0.0f;
+        int cnt = 0;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int o = L; o < 32; o <<= 1) acc[v] += __shfl_xor_sync(0xffffffffu, acc[v], o);
-        z = group_sum<32>(z);
-        cnt = __reduce_add_sync(0xffffffffu, cnt);
+        for (int v = 0; v < V; ++v) acc[v] = 0.0f;
+        sum_tokens<L, V, kVec>(a, ring, t_lo + warp * kGroups, t_hi, kBalWarps * kGroups, acc, z, cnt,
+                               [&](int id) { atomicAdd(&s_cnt[id], 1); });  // integers: any order
         if (lane == 0) {
             sh.z[warp] = z;
             sh.n[warp] = cnt;
         }
+        // the warps in order: the upper half's rows first go through shared memory to the lower
+        // half, which adds them and leaves its rows there
         float* mine = s_sum + (warp & (kBalSumRows - 1)) * E;
         if (warp >= kBalSumRows && lane < L)
 #pragma unroll
@@ -253,6 +391,7 @@ __device__ __forceinline__ void balance_stats(const BalanceArgs& a, int n, float
         if (threadIdx.x == 0) {
             float zs = 0.0f;
             int ns = 0;
+#pragma unroll
             for (int w = 0; w < kBalWarps; ++w) {
                 zs += sh.z[w];
                 ns += sh.n[w];
@@ -260,65 +399,88 @@ __device__ __forceinline__ void balance_stats(const BalanceArgs& a, int n, float
             a.slot_z[slot] = zs;
             a.slot_n[slot] = ns;
         }
+        if (--longs == 0) break;
         __syncthreads();
     }
 }
 
-// Adds the slots of a sequence for 32 experts; `item` is one (sequence, 32 experts) of the
-// num_seqs * ceil(E / 32) that `size` blocks share.
+// Adds the slots of sequence s for 32 experts: an item is one (sequence, 32 experts) of the
+// num_seqs * ceil(E / 32), which the cluster's warps share in groups of kGroup.  kGroup == 1 needs
+// no meeting of warps.
+template <int kGroup>
 __device__ __forceinline__ void finish_items(const BalanceArgs& a, int n, int rank, int size, FinishShared& sh) {
-    const int E = a.E, S = a.num_seqs;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    const int col_blocks = (E + kFinCols - 1) / kFinCols;
+    const int E = a.E;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per_block = (int)(blockDim.x >> 5) / kGroup;  // items a block has at once
+    const int member = warp % kGroup;
+    const int col_blocks = (E + kFinCols - 1) / kFinCols, items = a.num_seqs * col_blocks;
     const int chunk = (n + a.blocks - 1) / a.blocks;
-    for (int it = rank; it < S * col_blocks; it += size) {
-        const int s = it / col_blocks, cb = it - s * col_blocks;
+    for (int i0 = rank * per_block; i0 < items; i0 += size * per_block) {  // uniform over the block
+        const int it = i0 + warp / kGroup;
+        const bool on = it < items;
+        const int s = on ? it / col_blocks : 0, cb = it - s * col_blocks;
         const int e = cb * kFinCols + lane;
         const int sb = seq_begin(a.seq_off, s, n), se = seq_begin(a.seq_off, s + 1, n);
         // blocks that met the sequence
-        const int b0 = se > sb ? sb / chunk : 0, b1 = se > sb ? (se - 1) / chunk + 1 : 0;
-        float p = 0.0f;
-        int c = 0;
-        if (e < E)
-#pragma unroll 8
-            for (int b = b0 + warp; b < b1; b += warps) {
-                const size_t at = (size_t)(b + s) * E + e;
-                p += __ldcg(a.slot_p + at);
-                c += __ldcg(a.slot_c + at);
+        const int b0 = se > sb ? sb / chunk : 0, b1 = on && se > sb ? (se - 1) / chunk + 1 : 0;
+        float p = 0.0f, z = 0.0f;
+        int c = 0, m = 0;
+        if (cb == 0)
+            for (int b = b0 + member * 32 + lane; b < b1; b += 32 * kGroup) {
+                z += __ldcg(a.slot_z + b + s);
+                m += __ldcg(a.slot_n + b + s);
             }
-        sh.p[warp][lane] = p;
-        sh.c[warp][lane] = c;
-        __syncthreads();
-        if (warp == 0) {
-            p = 0.0f;
-            c = 0;
-#pragma unroll 8
-            for (int w = 0; w < warps; ++w) {
-                p += sh.p[w][lane];
-                c += sh.c[w][lane];
+        for (int b = b0 + member; b < b1; b += kBatch * kGroup) {  // kBatch slots on their way at once
+            float pv[kBatch];
+            int cv[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                const size_t at = (size_t)(b + i * kGroup + s) * E + e;
+                const bool in = e < E && b + i * kGroup < b1;
+                pv[i] = in ? __ldcg(a.slot_p + at) : 0.0f;
+                cv[i] = in ? __ldcg(a.slot_c + at) : 0;
             }
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) {
+                p += pv[i];
+                c += cv[i];
+            }
+        }
+        z = group_sum<32>(z);
+        m = __reduce_add_sync(0xffffffffu, m);
+        if (kGroup > 1) {
+            sh.p[warp][lane] = p;
+            sh.c[warp][lane] = c;
+            if (lane == 0) {
+                sh.z[warp] = z;
+                sh.n[warp] = m;
+            }
+            __syncthreads();
+            if (member == 0) {
+#pragma unroll
+                for (int w = 1; w < kGroup; ++w) {
+                    p += sh.p[warp + w][lane];
+                    c += sh.c[warp + w][lane];
+                    z += sh.z[warp + w];
+                    m += sh.n[warp + w];
+                }
+            }
+        }
+        if (on && member == 0) {
             if (e < E) {
                 a.prob_sums[(size_t)s * E + e] = p;
                 a.counts[(size_t)s * E + e] = c;
             }
             const float dot = group_sum<32>(e < E ? (float)c * p : 0.0f);
-            if (lane == 0) a.seq_dot[it] = dot;
-        }
-        if (warp == 1 && cb == 0) {
-            float z = 0.0f;
-            int m = 0;
-            for (int b = b0 + lane; b < b1; b += 32) {
-                z += __ldcg(a.slot_z + b + s);
-                m += __ldcg(a.slot_n + b + s);
-            }
-            z = group_sum<32>(z);
-            m = __reduce_add_sync(0xffffffffu, m);
             if (lane == 0) {
-                a.seq_z[s] = z;
-                a.seq_n[s] = m;
+                a.seq_dot[it] = dot;
+                if (cb == 0) {
+                    a.seq_z[s] = z;
+                    a.seq_n[s] = m;
+                }
             }
         }
-        __syncthreads();
+        if (kGroup > 1) __syncthreads();
     }
 }
 
@@ -326,53 +488,73 @@ __device__ __forceinline__ void finish_items(const BalanceArgs& a, int n, int ra
 // every blockDim-th sequence, and the threads' sums are added in a fixed order.
 __device__ __forceinline__ void finish_total(const BalanceArgs& a, FinishShared& sh) {
     const int S = a.num_seqs, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int used = min(warps, (S + 31) / 32);  // warps that have a sequence
     const int col_blocks = (a.E + kFinCols - 1) / kFinCols;
-    int filled = 0, total = 0;
-    double z = 0.0;
-    for (int s = threadIdx.x; s < S; s += blockDim.x) {
+    if (used == 1 && warp > 0) return;  // one warp does it, and meets nobody
+    auto dot_of = [&](int s) {
+        float dot = 0.0f;
+        for (int cb = 0; cb < col_blocks; cb += kBatch) {
+            float v[kBatch];
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i)
+                v[i] = cb + i < col_blocks ? __ldcg(a.seq_dot + (size_t)s * col_blocks + cb + i) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < kBatch; ++i) dot += v[i];
+        }
+        return dot;
+    };
+    // this thread's first sequence in registers
+    const bool mine = (int)threadIdx.x < S;
+    const int m0 = mine ? __ldcg(a.seq_n + threadIdx.x) : 0;
+    float z = mine ? __ldcg(a.seq_z + threadIdx.x) : 0.0f;
+    const float dot0 = mine ? dot_of(threadIdx.x) : 0.0f;
+    int filled = m0 > 0, total = m0;
+    for (int s = threadIdx.x + blockDim.x; s < S; s += blockDim.x) {
         const int m = __ldcg(a.seq_n + s);
         filled += m > 0;
         total += m;
-        z += (double)__ldcg(a.seq_z + s);
+        z += __ldcg(a.seq_z + s);
     }
     filled = __reduce_add_sync(0xffffffffu, filled);
     total = __reduce_add_sync(0xffffffffu, total);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    if (lane == 0) {
-        sh.i[warp] = filled;
-        sh.j[warp] = total;
-        sh.b[warp] = z;
+    z = group_sum<32>(z);
+    if (used > 1) {
+        if (lane == 0) {
+            sh.i[warp] = filled;
+            sh.j[warp] = total;
+            sh.z[warp] = z;
+        }
+        __syncthreads();
+        filled = total = 0;
+        z = 0.0f;
+        for (int w = 0; w < used; ++w) {
+            filled += sh.i[w];
+            total += sh.j[w];
+            z += sh.z[w];
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    filled = total = 0;
-    z = 0.0;
-    const int used = min(warps, (S + 31) / 32);  // the other warps' sums are 0
-    for (int w = 0; w < used; ++w) {
-        filled += sh.i[w];
-        total += sh.j[w];
-        z += sh.b[w];
-    }
-    double loss = 0.0;
+    const float scale = a.balance_coef * (float)a.E / ((float)max(filled, 1) * (float)a.k);
+    float loss = 0.0f;
     for (int s = threadIdx.x; s < S; s += blockDim.x) {
-        const double m = (double)__ldcg(a.seq_n + s);
-        const double as = m > 0.0 ? (double)a.balance_coef * a.E / ((double)filled * a.k * m * m) : 0.0;
-        double dot = 0.0;
-        for (int cb = 0; cb < col_blocks; ++cb) dot += (double)__ldcg(a.seq_dot + (size_t)s * col_blocks + cb);
-        if (m > 0.0) loss += as * dot;
-        a.grad_scales[s] = (float)as;
+        const bool first = s == (int)threadIdx.x;
+        const int m = first ? m0 : __ldcg(a.seq_n + s);
+        const float as = m > 0 ? scale / (float)m / (float)m : 0.0f;
+        if (m > 0) loss = fmaf(as, first ? dot0 : dot_of(s), loss);
+        a.grad_scales[s] = as;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) loss += __shfl_xor_sync(0xffffffffu, loss, o);
-    if (lane == 0) sh.a[warp] = loss;
-    __syncthreads();
+    loss = group_sum<32>(loss);
+    if (used > 1) {
+        if (lane == 0) sh.z[warp] = loss;
+        __syncthreads();
+        loss = 0.0f;
+        for (int w = 0; w < used; ++w) loss += sh.z[w];
+    }
     if (threadIdx.x == 0) {
-        loss = 0.0;
-        for (int w = 0; w < used; ++w) loss += sh.a[w];
-        const double zt = total > 0 ? (double)a.z_coef / total : 0.0;
-        a.losses[0] = (float)loss;
-        a.losses[1] = (float)(total > 0 ? zt * z : 0.0);
-        a.grad_scales[S] = (float)(2.0 * zt);
+        const float zt = total > 0 ? a.z_coef / (float)total : 0.0f;
+        a.losses[0] = loss;
+        a.losses[1] = total > 0 ? zt * z : 0.0f;
+        a.grad_scales[S] = 2.0f * zt;
     }
 }
 
@@ -380,33 +562,46 @@ __device__ __forceinline__ void finish_total(const BalanceArgs& a, FinishShared&
 // the totals; else balance_finish_kernel does the rest.
 template <int L, int V, bool kVec, bool kOne>
 __global__ void __launch_bounds__(kBalThreads, 1) balance_stats_kernel(const BalanceArgs a) {
-    extern __shared__ float s_bal[];  // [kBalSumRows][E] sums, then [E] counts
+    extern __shared__ __align__(16) float s_bal[];  // the warps' rings, [kBalSumRows][E] sums, [E] counts
     __shared__ StatsShared sh;
-    pdl_trigger();
     pdl_wait();
+    pdl_trigger();  // after the wait: the finishing kernel reads sizes and offsets before its own
     const int n = clamp_live(a.live, a.max_live);
     if (!kOne && blockIdx.x == 0 && threadIdx.x == 0) *a.ticket = 0u;
-    balance_stats<L, V, kVec>(a, n, s_bal, reinterpret_cast<int*>(s_bal + kBalSumRows * a.E), sh);
+    constexpr int kRingFloats = kRingOf<V> * 32 * V;  // of a warp
+    float* s_sum = s_bal + kBalWarps * kRingFloats;
+    balance_stats<L, V, kVec>(a, n, s_bal + (threadIdx.x >> 5) * kRingFloats, s_sum,
+                              reinterpret_cast<int*>(s_sum + kBalSumRows * a.E), sh);
     if constexpr (kOne) {
         __shared__ FinishShared fin;
         cluster_sync();  // the slots of every block are written
-        finish_items(a, n, blockIdx.x, gridDim.x, fin);
+        finish_items<1>(a, n, blockIdx.x, gridDim.x, fin);
         cluster_sync();
         if (blockIdx.x == 0) finish_total(a, fin);
     }
 }
 
+// kCluster: one cluster, which meets in its own barrier; else (many sequences or experts) any number
+// of blocks, the last of which to come to the ticket does the totals.
+template <bool kCluster>
 __global__ void __launch_bounds__(kFinThreads) balance_finish_kernel(const BalanceArgs a) {
     __shared__ FinishShared fin;
     __shared__ int s_last;
     pdl_trigger();
+    // the kernel before this one waited before it released this one: sizes and offsets are there
+    const int n = clamp_live(a.live, a.max_live);
     pdl_wait();
-    finish_items(a, clamp_live(a.live, a.max_live), blockIdx.x, gridDim.x, fin);
+    finish_items<kFinGroup>(a, n, blockIdx.x, gridDim.x, fin);
+    if (kCluster) {
+        cluster_sync();
+        if (blockIdx.x == 0) finish_total(a, fin);
+        return;
+    }
     __threadfence();
     __syncthreads();
     if (threadIdx.x == 0) s_last = atomicAdd(a.ticket, 1u) == gridDim.x - 1 ? 1 : 0;
     __syncthreads();
-    if (!s_last) return;  // the last block to finish has every sequence's sums
+    if (!s_last) return;
     __threadfence();
     finish_total(a, fin);
 }
@@ -426,22 +621,22 @@ struct RouteGradArgs {
     float* dlogits;
 };
 
-// A group of lanes per token, as the forward: the losses' part in registers; the chosen part
-// is added to the row in shared memory, in route order (an expert named twice gets both adds in
-// that order), from where the whole row leaves in wide stores.  Route j of a token belongs to
-// lane j % L of its group.
+// A group of lanes per token, as the forward: the losses' part in registers; the chosen part is
+// added to the row in its ring slot, from where the whole row leaves in wide stores.  Route j of a
+// token belongs to lane j % L of its group; routes of different experts add in any order, an
+// expert named twice (and any, where there are more routes than lanes) in route order.
 template <int L, int V, bool kVec>
-__global__ void __launch_bounds__(kGradThreads) route_backward_kernel(const RouteGradArgs a) {
-    extern __shared__ __align__(16) float s_row_all[];
+__global__ void __launch_bounds__(kGradThreads, kGradBlocks<V>) route_backward_kernel(const RouteGradArgs a) {
+    extern __shared__ __align__(16) float s_rings[];
     constexpr int kGroups = 32 / L;
     constexpr int kSlots = (kMaxTopK + L - 1) / L;  // routes of a lane
+    constexpr int kSlot = 32 * V, kRing = kRingOf<V>;
     pdl_trigger();
     pdl_wait();
     const int E = a.E, k = a.k;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int gl = lane & (L - 1), g = warp * kGroups + lane / L;
-    const int pitch = (E + 3) & ~3;
-    float* s_row = s_row_all + (size_t)g * pitch;
+    const int gl = lane & (L - 1), group = lane / L;
+    float* ring = s_rings + warp * kRing * kSlot;
     const int n = clamp_live(a.live, a.max_live);
     const bool has_loss = a.counts != nullptr;
     const float g0 = a.grad_losses != nullptr ? __ldg(a.grad_losses) : 1.0f;
@@ -455,26 +650,21 @@ __global__ void __launch_bounds__(kGradThreads) route_backward_kernel(const Rout
     const int chunk = (n + a.blocks - 1) / a.blocks;
     const int c0 = min(n, (int)blockIdx.x * chunk), c1 = min(n, c0 + chunk);
     constexpr int kStep = kGradWarps * kGroups;
-    int t = c0 + warp * kGroups + lane / L;
+    int t = c0 + warp * kGroups + group;
     auto lse_of = [&](int tt) {
         return tt < c1 ? (a.lse != nullptr ? __ldg(a.lse + tt) : 0.0f) : -INFINITY;
     };
     float lse_next = lse_of(t);
-    float next[V];
-    if (has_loss) load_row<L, V, kVec>(a.logits + (size_t)t * E, E, gl, t < c1, -INFINITY, next);
+#pragma unroll
+    for (int i = 0; i < kRing - 1; ++i)
+        ring_request<L, V, kVec>(ring + i * kSlot, a.logits + (size_t)(t + i * kStep) * E, E, gl,
+                                 has_loss && t + i * kStep < c1);
+    int slot = 0;
     for (int tw = c0 + warp * kGroups; tw < c1; tw += kStep, t += kStep) {
         const bool in = t < c1;
         const float lse = lse_next;
         const bool counted = lse != -INFINITY;  // true for NaN
-        float x[V];
-        if (has_loss) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) x[v] = next[v];
-        }
-        // the next token's row and this one's routes are on their way meanwhile
         lse_next = lse_of(t + kStep);
-        if (has_loss)
-            load_row<L, V, kVec>(a.logits + (size_t)(t + kStep) * E, E, gl, t + kStep < c1, -INFINITY, next);
         int id[kSlots];
         float w[kSlots], d[kSlots];
         if (a.dprobs != nullptr) {
@@ -491,7 +681,12 @@ __global__ void __launch_bounds__(kGradThreads) route_backward_kernel(const Rout
                 }
             }
         }
+        float* row = ring + slot * kSlot;
+        const int refill = slot + kRing - 1 < kRing ? slot + kRing - 1 : slot - 1;
+        float x[V];
+        ring_wait<kRing>();
         if (has_loss) {
+            ring_read<L, V, kVec>(row, E, gl, counted, x);
             if (counted && (t < s_lo || t >= s_hi)) {
                 int s = find_seq(a.seq_off, a.num_seqs, t);
                 s = s < a.num_seqs ? s : a.num_seqs - 1;
@@ -531,57 +726,30 @@ __global__ void __launch_bounds__(kGradThreads) route_backward_kernel(const Rout
 #pragma unroll
             for (int r = 0; r < kSlots; ++r) wd = fmaf(w[r], d[r], wd);
             wd = group_sum<L>(wd);
-            if (kVec) {
-#pragma unroll
-                for (int q = 0; q < V / 4; ++q) {
-                    const int c = q * (4 * L) + gl * 4;
-                    if (c < E)
-                        *reinterpret_cast<float4*>(s_row + c) = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2],
-                                                                            x[4 * q + 3]);
-                }
-            } else {
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (v * L + gl < E) s_row[v * L + gl] = x[v];
-            }
-            __syncwarp();
-            // routes of different experts add in any order; an expert named twice, or more routes
-            // than lanes: one route after another
+            ring_write<V, kVec>(row, x);
             bool apart = k <= L;
             if (apart) {
-                const unsigned key = id[0] >= 0 ? (unsigned)(id[0] * kGroups + lane / L) : 0x80000000u + lane;
+                const unsigned key = id[0] >= 0 ? (unsigned)(id[0] * kGroups + group) : 0x80000000u + lane;
                 apart = __all_sync(0xffffffffu, __popc(__match_any_sync(0xffffffffu, key)) == 1);
             }
+            __syncwarp();
             if (apart) {
-                if (id[0] >= 0) s_row[id[0]] += w[0] * (d[0] - wd);
+                if (id[0] >= 0) row[ring_place<L, kVec>(id[0], group)] += w[0] * (d[0] - wd);
                 __syncwarp();
             } else {
 #pragma unroll
                 for (int r = 0; r < kSlots; ++r)
                     for (int j = r * L; j < min(k, r * L + L); ++j) {
-                        if (gl == j - r * L && id[r] >= 0) s_row[id[r]] += w[r] * (d[r] - wd);
+                        if (gl == j - r * L && id[r] >= 0)
+                            row[ring_place<L, kVec>(id[r], group)] += w[r] * (d[r] - wd);
                         __syncwarp();
                     }
             }
-            if (kVec) {
-#pragma unroll
-                for (int q = 0; q < V / 4; ++q) {
-                    const int c = q * (4 * L) + gl * 4;
-                    if (c < E) {
-                        const float4 f = *reinterpret_cast<const float4*>(s_row + c);
-                        x[4 * q] = f.x;
-                        x[4 * q + 1] = f.y;
-                        x[4 * q + 2] = f.z;
-                        x[4 * q + 3] = f.w;
-                    }
-                }
-            } else {
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    if (v * L + gl < E) x[v] = s_row[v * L + gl];
-            }
-            __syncwarp();
+            ring_read<L, V, kVec>(row, E, gl, true, x);  // columns from E on are not stored
         }
+        ring_request<L, V, kVec>(ring + refill * kSlot, a.logits + (size_t)(t + (kRing - 1) * kStep) * E, E, gl,
+                                 has_loss && t + (kRing - 1) * kStep < c1);
+        slot = slot + 1 == kRing ? 0 : slot + 1;
         if (in) {
             float* out = a.dlogits + (size_t)t * E;
             if (kVec) {
@@ -599,6 +767,7 @@ __global__ void __launch_bounds__(kGradThreads) route_backward_kernel(const Rout
             }
         }
     }
+    ring_drain();
 }
 
 // Tokens that a warp holds at once (32 / L, as by_width picks L).
@@ -663,34 +832,67 @@ cudaError_t by_width(int E, bool vec, const Args& a, cudaStream_t s) {
 #undef MOE_BY_WIDTH
 }
 
+// Dynamic shared memory over 48 KB is asked for once per kernel and device.
+template <class Kernel>
+cudaError_t allow_smem(Kernel kern, size_t bytes, bool (&done)[64]) {
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (done[dev]) return cudaSuccess;
+    err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (err == cudaSuccess) done[dev] = true;
+    return err;
+}
+
+// A launch of one cluster of `blocks` blocks.
+template <class... KArgs, class... Args>
+cudaError_t launch_cluster(void (*kern)(KArgs...), int blocks, int threads, size_t smem, cudaStream_t s,
+                           Args&&... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)blocks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)blocks);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+    return err != cudaSuccess ? err : cudaGetLastError();
+}
+
 template <int L, int V, bool kVec>
 struct LaunchStats {
+    static constexpr size_t smem(int E) {
+        return (size_t)(kBalWarps * kRingOf<V> * 32 * V + (kBalSumRows + 1) * E) * 4;
+    }
     static cudaError_t go(const BalanceArgs& a, cudaStream_t s) {
-        const size_t smem = (size_t)(kBalSumRows + 1) * a.E * 4;  // at most 36 KB
-        if (a.blocks > kClusterBlocks)
-            return launch_dependent(balance_stats_kernel<L, V, kVec, false>, dim3(a.blocks), dim3(kBalThreads), smem, s,
-                                    a);
-        cudaLaunchAttribute attr[2];
-        attr[0].id = cudaLaunchAttributeClusterDimension;
-        attr[0].val.clusterDim.x = (unsigned)a.blocks;
-        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-        attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[1].val.programmaticStreamSerializationAllowed = 1;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(a.blocks);
-        cfg.blockDim = dim3(kBalThreads);
-        cfg.dynamicSmemBytes = smem;
-        cfg.stream = s;
-        cfg.attrs = attr;
-        cfg.numAttrs = 2;
-        const cudaError_t err = cudaLaunchKernelEx(&cfg, balance_stats_kernel<L, V, kVec, true>, a);
-        return err != cudaSuccess ? err : cudaGetLastError();
+        static_assert(smem(L * V) + sizeof(FinishShared) + sizeof(StatsShared) + 1024 <= 232448, "shared memory budget");
+        static bool done[2][64];
+        const bool one = a.blocks <= kClusterBlocks;
+        const size_t most = smem(L * V);
+        cudaError_t err = one ? allow_smem(balance_stats_kernel<L, V, kVec, true>, most, done[1])
+                              : allow_smem(balance_stats_kernel<L, V, kVec, false>, most, done[0]);
+        if (err != cudaSuccess) return err;
+        if (one)
+            return launch_cluster(balance_stats_kernel<L, V, kVec, true>, a.blocks, kBalThreads, smem(a.E), s, a);
+        return launch_dependent(balance_stats_kernel<L, V, kVec, false>, dim3(a.blocks), dim3(kBalThreads), smem(a.E), s,
+                                a);
     }
 };
 template <int L, int V, bool kVec>
 struct LaunchBackward {
-    static cudaError_t go(const RouteGradArgs& a, cudaStream_t s) {
-        const size_t smem = a.dprobs != nullptr ? (size_t)kGradWarps * (32 / L) * ((a.E + 3) & ~3) * 4 : 0;  // <= 32 KB
+    static cudaError_t go(RouteGradArgs a, cudaStream_t s) {
+        a.blocks = blocks_for(a.max_live, kGradWarps * (32 / L), (long long)num_sms() * kGradBlocks<V>);
+        constexpr size_t smem = (size_t)kGradWarps * kRingOf<V> * 32 * V * 4;  // at most 64 KB
+        static bool done[64];
+        const cudaError_t err = allow_smem(route_backward_kernel<L, V, kVec>, smem, done);
+        if (err != cudaSuccess) return err;
         return launch_dependent(route_backward_kernel<L, V, kVec>, dim3(a.blocks), dim3(kGradThreads), smem, s, a);
     }
 };
@@ -753,9 +955,14 @@ moe_status moe_balance_loss(const moe_plan* plan, const float* logits, const int
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     if (a.blocks <= kClusterBlocks) return MOE_OK;
     const long long items = (long long)num_seqs * ((a.E + kFinCols - 1) / kFinCols);
-    const long long cap = (long long)num_sms() * 2;
-    e = launch_dependent(balance_finish_kernel, dim3((unsigned)(items < cap ? items : cap)), dim3(kFinThreads), 0, s,
-                         a);
+    constexpr int kPerBlock = kFinWarps / kFinGroup;
+    if (items <= 2 * kFinBlocks * kPerBlock) {
+        e = launch_cluster(balance_finish_kernel<true>, kFinBlocks, kFinThreads, 0, s, a);
+    } else {
+        const long long want = (items + kPerBlock - 1) / kPerBlock, cap = num_sms();
+        e = launch_dependent(balance_finish_kernel<false>, dim3((unsigned)(want < cap ? want : cap)),
+                             dim3(kFinThreads), 0, s, a);
+    }
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -781,7 +988,6 @@ moe_status moe_route_backward(const moe_plan* plan, const float* logits, const i
     a.E = plan->d.num_experts;
     a.k = plan->d.top_k;
     a.num_seqs = num_seqs;
-    a.blocks = blocks_for(plan->max_live, kGradWarps * tokens_per_warp(a.E), (long long)num_sms() * 4);
     a.lse = lse;
     a.counts = counts;
     a.grad_scales = grad_scales;
