@@ -163,24 +163,33 @@ __device__ __forceinline__ void ring_wait() {  // the oldest of kRing - 1 reques
     asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
 }
 __device__ __forceinline__ void ring_drain() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-// The lane's V values of a row; columns from E on, and all of an absent row, read as -infinity.
+// The lane's V values of a row, as the slot has them.
+template <int V, bool kVec>
+__device__ __forceinline__ void ring_read(const float* slot, float (&x)[V]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        if (kVec) {
+            if (v % 4 == 0) {
+                const float4 f = *reinterpret_cast<const float4*>(slot + (v / 4 * 32 + lane) * 4);
+                x[v] = f.x;
+                x[v + 1] = f.y;
+                x[v + 2] = f.z;
+                x[v + 3] = f.w;
+            }
+        } else {
+            x[v] = slot[v * 32 + lane];
+        }
+    }
+}
+// The same with -infinity in columns from E on, and in all of a row that was not requested.
 template <int L, int V, bool kVec>
 __device__ __forceinline__ void ring_read(const float* slot, int E, int gl, bool have, float (&x)[V]) {
-    const int lane = threadIdx.x & 31;
-    if (kVec) {
+    ring_read<V, kVec>(slot, x);
+    if (E == L * V && __all_sync(0xffffffffu, have)) return;
 #pragma unroll
-        for (int q = 0; q < V / 4; ++q) {
-            const float4 f = *reinterpret_cast<const float4*>(slot + (q * 32 + lane) * 4);
-            const bool in = have && q * (4 * L) + gl * 4 < E;
-            x[4 * q] = in ? f.x : -INFINITY;
-            x[4 * q + 1] = in ? f.y : -INFINITY;
-            x[4 * q + 2] = in ? f.z : -INFINITY;
-            x[4 * q + 3] = in ? f.w : -INFINITY;
-        }
-    } else {
-#pragma unroll
-        for (int v = 0; v < V; ++v) x[v] = have && v * L + gl < E ? slot[v * 32 + lane] : -INFINITY;
-    }
+    for (int v = 0; v < V; ++v)
+        if (!(have && col_of<L, kVec>(v, gl) < E)) x[v] = -INFINITY;
 }
 // Writes the lane's values back to its places.
 template <int V, bool kVec>
@@ -207,6 +216,13 @@ __device__ __forceinline__ float exp2_approx(float x) {  // 2 ulp; 0 for -infini
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
+}
+
+// x = exp(x - mx).  The difference first: near the type's bounds a product with log2(e) overflows.
+template <int V>
+__device__ __forceinline__ void exp_terms(float (&x)[V], float mx) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) x[v] = exp2_approx((x[v] - mx) * kLog2e);
 }
 
 struct StatsShared {
@@ -255,12 +271,10 @@ __device__ __forceinline__ void sum_tokens(const BalanceArgs& a, float* ring, in
         for (int v = 0; v < V; ++v) mx = fmaxf(mx, x[v]);
         mx = group_max<L>(mx);
         if (mx == -INFINITY) mx = 0.0f;  // all -infinity: the sum below is 0 (NaN with a NaN logit)
+        exp_terms<V>(x, mx);
         float sum = 0.0f;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            x[v] = exp2_approx((x[v] - mx) * kLog2e);  // the difference first: rows near the type's bounds
-            sum += x[v];
-        }
+        for (int v = 0; v < V; ++v) sum += x[v];
         sum = group_sum<L>(sum);
         const bool counted = have[0] && sum != 0.0f;  // true for NaN: it shows in the losses
         const float inv = counted ? __frcp_rn(sum) : 0.0f;
@@ -704,19 +718,21 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocks<V>) route_backward_k
 #pragma unroll
             for (int v = 0; v < V; ++v) mx = fmaxf(mx, x[v]);
             mx = group_max<L>(mx);
+            if (mx == -INFINITY) mx = 0.0f;
+            exp_terms<V>(x, mx);
             float sum = 0.0f, dot = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                x[v] = exp2_approx((x[v] - mx) * kLog2e);
                 sum += x[v];
                 dot = fmaf(cnt[v], x[v], dot);
             }
             sum = group_sum<L>(sum);
             dot = group_sum<L>(dot);
-            const float inv = __frcp_rn(sum);
-            const float base = fmaf(zs, lse, -as * (dot * inv));  // as * (c - <c, p>) + zs * lse
+            // p (as (c - <c, p>) + zs lse), with p = x / sum; 0 where the token does not count
+            const float inv = counted ? __frcp_rn(sum) : 0.0f;
+            const float slope = as * inv, base = counted ? fmaf(zs, lse, -as * (dot * inv)) * inv : 0.0f;
 #pragma unroll
-            for (int v = 0; v < V; ++v) x[v] = counted ? x[v] * inv * fmaf(as, cnt[v], base) : 0.0f;
+            for (int v = 0; v < V; ++v) x[v] *= fmaf(slope, cnt[v], base);
         } else {
 #pragma unroll
             for (int v = 0; v < V; ++v) x[v] = 0.0f;
@@ -745,7 +761,7 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocks<V>) route_backward_k
                         __syncwarp();
                     }
             }
-            ring_read<L, V, kVec>(row, E, gl, true, x);  // columns from E on are not stored
+            ring_read<V, kVec>(row, x);  // columns from E on are not stored
         }
         ring_request<L, V, kVec>(ring + refill * kSlot, a.logits + (size_t)(t + (kRing - 1) * kStep) * E, E, gl,
                                  has_loss && t + (kRing - 1) * kStep < c1);
