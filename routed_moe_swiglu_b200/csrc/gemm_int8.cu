@@ -176,7 +176,7 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bars->acc_full[b], 1);
-            mbar_init(&bars->acc_empty[b], 2 * kEpiWarps);
+            mbar_init(&bars->acc_empty[b], 2 * kEpiWarps * (kMode == kDown ? 1 : kEpiGroups));
         }
         mbar_init(&bars->done, 1);
         bars->abort_flag = 0;
@@ -373,15 +373,17 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
         }
         __syncwarp();
     } else {
-        // ---------------- epilogue: warps 2..17, in two groups of eight that take the pair's tiles in
-        // turn (one accumulator each), so that one group's stores overlap the other's arithmetic; a
-        // pair with one tile at most shares it among both.  TMEM lanes are weight rows (output
+        // ---------------- epilogue: warps 2..17, in two groups of eight.  The down GEMM, whose stores
+        // take longest, gives the groups the pair's tiles in turn (one accumulator each); the others
+        // share each tile among both, which frees its accumulator sooner (65,536 routes: gate/up 297 us
+        // shared, 309 in turn; down 178 and 174).  A pair with one tile at most always shares it.
+        // TMEM lanes are weight rows (output
         // columns), TMEM columns activation rows: a lane's weight scale is a register, a row's scale
         // comes from shared memory, and the 32 lanes' stores of one row are neighbours.  The next
         // tile's scales are fetched while this one is drained.
         const int ew = (warp - 2) & (kEpiWarps - 1), group = (warp - 2) / kEpiWarps;
         const int quad = warp & 3;  // TMEM lane quarter this warp may read
-        const bool share = total_tiles <= npairs;
+        const bool share = kMode != kDown || total_tiles <= npairs;
         // this warp takes the chunks c = c0, c0 + cs, ... of kChunk columns
         const int c0 = (ew >> 2) + (share ? 2 * group : 0), cs = share ? 4 : 2;
         const int step = share ? npairs : kEpiGroups * npairs;
