@@ -316,7 +316,7 @@ cudaError_t launch_int8_quantize_rows(const __nv_bfloat16* in, long long rows, i
     return by_row(warp_per_row(rows, cols / 8), cols / 8, [&](auto warps, auto held) {
         constexpr int kRows = 4 / warps.value;
         return launch_dependent(int8_quantize_rows_kernel<warps.value, held.value>,
-                                dim3(capped_grid((rows + kRows - 1) / kRows, 16)), dim3(kI8Threads), 0, s,
+                                dim3(capped_grid((rows + kRows - 1) / kRows, 64)), dim3(kI8Threads), 0, s,
                                 reinterpret_cast<const uint4*>(in), rows, cols / 8, ld_in / 8, live,
                                 reinterpret_cast<uint2*>(q), scales);
     });
@@ -337,7 +337,7 @@ cudaError_t launch_quantize_h_int8(const __nv_bfloat16* h, const int* live, int 
     return by_row(warp_per_row(rows, fp / 8), fp / 8, [&](auto warps, auto held) {
         constexpr int kRows = 4 / warps.value;
         return launch_dependent(quantize_h_int8_kernel<warps.value, held.value>,
-                                dim3(capped_grid((rows + kRows - 1) / kRows, 16)), dim3(kI8Threads), 0, s,
+                                dim3(capped_grid((rows + kRows - 1) / kRows, 64)), dim3(kI8Threads), 0, s,
                                 reinterpret_cast<const uint4*>(h), live, max_live, k, fp, inv,
                                 reinterpret_cast<uint2*>(hq), hs, status);
     });
