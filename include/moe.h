@@ -563,7 +563,9 @@ moe_status moe_ep_ipc_close(void* dev_ptr);
  *           (r % 32) * 16 + (r / 32) * 4 + b.  NVFP4 h and xq are codes two
  *           per byte ([rows_padded, ceil(K/256)*128] bytes).
  *   xq_row_scales, h_row_scales  NVFP4: fp32 second-level scale per padded row;
- *           int8: the row's scale (else NULL);  h_fp32  the gate/up GEMM's fp32 h rows before
+ *           int8: the row's scale (else NULL).  int8 plans of at most four
+ *           live rows quantise x and h inside the products and write neither xq, h
+ *           nor these scales;  h_fp32  the gate/up GEMM's fp32 h rows before
  *           quantisation: NVFP4 [rows_padded, ceil(F/256)*256]; MXFP8 plans
  *           made with MOE_FLAG_KEEP_H_FP32 [rows_padded, ceil(F/128)*128];
  *           else NULL. */

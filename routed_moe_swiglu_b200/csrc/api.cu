@@ -340,6 +340,8 @@ static moe_status forward_impl(const moe_plan* plan, const void* x, const float*
     const bool fp8 = plan->d.precision == MOE_MXFP8;
     const bool fp4 = plan->d.precision == MOE_NVFP4;
     const bool i8 = plan->d.precision == MOE_INT8;
+    // int8 plans of very few tokens quantise x and h inside their products
+    const bool few = i8 && int8_gemv_experts(plan->max_live);
     const unsigned long long R = (unsigned long long)plan->rows_pad;
     const unsigned long long uH = (unsigned long long)H, uE = (unsigned long long)E;
     const CUtensorMapDataType dt = fp8 || fp4 || i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
@@ -370,6 +372,8 @@ static moe_status forward_impl(const moe_plan* plan, const void* x, const float*
                 !make_tensor_map(&rB2.m[i], dt, 3, ws + L.h, dH, sW2, box, CU_TENSOR_MAP_SWIZZLE_128B))
                 return MOE_ERR_CUDA;
         }
+    } else if (few) {
+        // no TMA
     } else if (i8) {
         // int8 (CTA pairs): K stage = 256 elements = two 128-byte swizzle atoms.  Weights are
         // blocks of [128 rows][128 codes], the blocks of a row block after one another along K;
@@ -458,7 +462,7 @@ static moe_status forward_impl(const moe_plan* plan, const void* x, const float*
         e = launch_gather_nvfp4(static_cast<const __nv_bfloat16*>(x), live_count_dev, max_live, H, (int)plan->hp, k,
                                 inv, ws + L.xq, ws + L.xs, reinterpret_cast<float*>(ws + L.xg), status, s);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
-    } else if (i8) {
+    } else if (i8 && !few) {
         e = launch_gather_int8(static_cast<const __nv_bfloat16*>(x), live_count_dev, max_live, H, (int)plan->hp, k, inv,
                                ws + L.xq, reinterpret_cast<float*>(ws + L.xg), status, s);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
@@ -485,12 +489,17 @@ static moe_status forward_impl(const moe_plan* plan, const void* x, const float*
         g.clamp = plan->d.gate_up_clamp;
         g.relu2 = (plan->d.flags & MOE_FLAG_SQUARED_RELU) != 0;
         if (!mark(3)) return MOE_ERR_CUDA;
-        e = launch_gemm1_int8(tA1, rB1, g, m_tiles * g.n_tiles, s);
+        const int max_tiles = (int)(plan->max_routes < E ? plan->max_routes : E);  // few: a tile an expert at most
+        const __nv_bfloat16* hf = reinterpret_cast<const __nv_bfloat16*>(ws + L.hf);
+        e = few ? launch_gemv1_int8(wb + plan->wb.w1, static_cast<const __nv_bfloat16*>(x), g, H, k, max_live, max_tiles,
+                                    s)
+                : launch_gemm1_int8(tA1, rB1, g, m_tiles * g.n_tiles, s);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
-        // h rows -> int8 with a scale per row (timed with the gate/up stage)
-        e = launch_quantize_h_int8(reinterpret_cast<const __nv_bfloat16*>(ws + L.hf), live_count_dev, max_live, k,
-                                   (int)plan->fp, inv, ws + L.h, reinterpret_cast<float*>(ws + L.hg), status, s);
-        if (e != cudaSuccess) return MOE_ERR_CUDA;
+        if (!few) {  // h rows -> int8 with a scale per row (timed with the gate/up stage)
+            e = launch_quantize_h_int8(hf, live_count_dev, max_live, k, (int)plan->fp, inv, ws + L.h,
+                                       reinterpret_cast<float*>(ws + L.hg), status, s);
+            if (e != cudaSuccess) return MOE_ERR_CUDA;
+        }
         g.out = ws + L.y;
         g.out_ld = g.out_cols = H;
         g.n_tiles = plan->nt2;
@@ -499,7 +508,8 @@ static moe_status forward_impl(const moe_plan* plan, const void* x, const float*
         g.row_scale = reinterpret_cast<const float*>(ws + L.hg);
         g.w_scale = reinterpret_cast<const float*>(wb + plan->wb.w2s);
         if (!mark(4)) return MOE_ERR_CUDA;
-        e = launch_gemm2_int8(tA2, rB2, g, m_tiles * g.n_tiles, s);
+        e = few ? launch_gemv2_int8(wb + plan->wb.w2, hf, g, plan->d.ffn, plan->fp, max_live, max_tiles, s)
+                : launch_gemm2_int8(tA2, rB2, g, m_tiles * g.n_tiles, s);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
     } else {
     GemmParams g1{};

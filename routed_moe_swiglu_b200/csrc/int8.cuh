@@ -91,6 +91,21 @@ __device__ __forceinline__ uint32_t int8_amax_pairs(uint4 v, uint32_t a) {
 // The larger of a pair, as the bits of an fp32.
 __device__ __forceinline__ uint32_t int8_amax_bits(uint32_t a) { return max(a << 16, a & 0xffff0000u); }
 
+// x clamped to [-c, c]; a NaN (a row that holds one) stays NaN.
+__device__ __forceinline__ float clamp_nan(float x, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;\n\tmin.NaN.f32 %0, %0, %3;" : "=f"(r) : "f"(x), "f"(-c), "f"(c));
+    return r;
+}
+// 1 / (1 + exp(-g)) from the approximate exponential and reciprocal (2^-22 and 1 ulp; the
+// exponent's rounding adds |g| 2^-24): far below the bf16 step that h is rounded to.
+__device__ __forceinline__ float sigmoid_approx(float g) {
+    float e, r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+    return r;
+}
+
 struct Int8Gemm {
     const int4* tiles;              // grouped: {expert, first padded row, valid rows, first permuted row}
     const unsigned* status_words;   // grouped: the workspace's status words
@@ -124,6 +139,14 @@ cudaError_t launch_gemm_dense_int8(const CUtensorMap& a, const BoxMaps8& b, cons
                                    cudaStream_t s);
 // Few tokens (gemm_int8_few.cu): bf16 rows quantised in the same launch, where they fit, or codes.
 int int8_split_for(long long tiles, int atoms);  // CTAs that share a tile's K
+// The expert products of very few tokens (gemv_int8.cu), which quantise x and h themselves: whether a
+// plan takes them, and the two products (w: the prepared weights; tokens:
+// the plan's most live rows; max_tiles: experts with a route at most).
+bool int8_gemv_experts(long long max_live);
+cudaError_t launch_gemv1_int8(const uint8_t* w, const __nv_bfloat16* x, const Int8Gemm& g, int hidden, int top_k,
+                              int tokens, int max_tiles, cudaStream_t s);
+cudaError_t launch_gemv2_int8(const uint8_t* w, const __nv_bfloat16* h, const Int8Gemm& g, int ffn, long long ld_h,
+                              int tokens, int max_tiles, cudaStream_t s);
 bool int8_few_fused_fits(long long rows, int cols_in, int cols_out);
 cudaError_t launch_int8_few_fused(const CUtensorMap& a, const __nv_bfloat16* x, long long ld_x, const Int8Gemm& g,
                                   int cols_in, cudaStream_t s);

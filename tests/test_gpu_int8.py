@@ -418,6 +418,63 @@ def test_every_tile_width():
     assert m.status() == 0
 
 
+@pytest.mark.parametrize("H,F,E,k,T,variant", [
+    (8, 8, 1, 1, 1, {}), (2688, 1856, 16, 6, 1, {}), (2048, 1024, 12, 8, 2, {}), (264, 136, 5, 2, 4, {}),
+    (1032, 520, 4, 4, 3, dict(out_dtype="bf16")), (328, 200, 6, 3, 4, dict(squared_relu=True)),
+    (328, 200, 6, 3, 2, dict(probs_in_fc1=True, gate_up_clamp=0.75)),
+    (136, 392, 7, 7, 4, dict(squared_relu=True, probs_in_fc1=True, gate_up_clamp=0.5)), (16384, 64, 2, 1, 4, {}),
+    (64, 16384, 2, 2, 3, {}), (264, 136, 5, 2, 5, {})])
+def test_few_tokens_are_bitwise_the_wide_products(H, F, E, k, T, variant):
+    """Plans of at most four live rows (x and h quantised inside the products) give the bits of plans of
+    many, in h, in y and in the output, at every live count."""
+    x, logits, weights = workloads.small_case(H, F, E, k, T, seed=H + F + T, capacity=T + 3)
+    few = GpuMoe(H, F, E, k, T + 3, weights, precision="int8", max_live=T, **variant)
+    x2, l2 = (torch.cat([t, t.new_full((300, t.shape[1]), float("nan"))]) for t in (x, logits))
+    wide = GpuMoe(H, F, E, k, T + 303, weights, precision="int8", **variant)
+    want = wide.forward(x2.cuda(), T, logits=l2.cuda())[:T].clone()
+    out = few.forward(x.cuda(), T, logits=logits.cuda())
+    assert torch.equal(out[:T], want) and torch.isnan(out[T:]).all() and few.status() == 0
+    views = few.views(), wide.views()
+    rows = [m.read_i32(v["inv"], T * k) for m, v in zip((few, wide), views)]
+    for name, n, dt in (("h_bf16", _pad128(F), torch.bfloat16), ("y", H, torch.float32)):
+        a, b = (_ws(m, v[name], v["rows_padded"] * n, dt).view(-1, n)[torch.from_numpy(r).long().cuda()]
+                for m, v, r in zip((few, wide), views, rows))
+        assert torch.equal(a, b), name
+    for n in {0, 1, T // 2, T - 1}:
+        out = few.forward(x.cuda(), n, logits=logits.cuda())
+        assert torch.equal(out[:n], want[:n]) and torch.isnan(out[n:]).all()
+
+
+def test_few_tokens_in_a_graph_with_bad_routes_and_nan():
+    """One capture of a plan of few rows serves every live count; a dropped token's row is zero, a
+    token with a NaN has a row of NaN, the others keep their bits."""
+    H, F, E, k, cap = 264, 136, 6, 2, 4
+    x, _, weights = workloads.small_case(H, F, E, k, cap, seed=23)
+    g = torch.Generator().manual_seed(2)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(cap)]).int()
+    probs = torch.softmax(torch.randn((cap, k), generator=g), dim=1)
+    m = GpuMoe(H, F, E, k, cap, weights, precision="int8")
+    xd, idd, pd = x.cuda(), ids.cuda(), probs.cuda()
+    good = m.forward(xd, cap, ids=idd, probs=pd).clone()
+    out = torch.zeros((cap, H), device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        rm.moe_forward(m.plan, xd, m.wbuf, m.live, out, m.ws, ids=idd, probs=pd)
+    xd[1, 40] = float("inf")
+    idd[2, 1] = E
+    for n in (4, 1, 0, 3, 2, 9):
+        out.fill_(-7.0)
+        m.live.fill_(n)
+        graph.replay()
+        n = min(n, cap)
+        keep = [t for t in range(n) if t not in (1, 2)]
+        assert torch.equal(out[keep], good[keep]) and (out[n:] == -7.0).all()
+        if n > 1:
+            assert torch.isnan(out[1]).all()
+        if n > 2:
+            assert (out[2] == 0).all()
+
+
 def test_a_token_of_nan_stays_alone():
     """A NaN or an infinity in one token's row makes that token's output NaN (clamped or not) and
     changes no other token."""
