@@ -100,7 +100,18 @@ __device__ __forceinline__ StageCfg stage_cfg(int widest_tile) {
 
 enum { kGateUp = 0, kDown = 1, kDense = 2 };
 
-// Tile t of the launch: {expert, first activation row, valid rows, first permuted row}.
+// The row tile (x) and weight tile (y) of tile t.  Blocks of p.raster row tiles are walked weight tile
+// by weight tile; with 1 (grouped: always) a row tile's weight tiles follow one another.
+template <int kMode>
+__device__ __forceinline__ int2 place_of(const Int8Gemm& p, int num_m, int t) {
+    const int raster = kMode == kDense ? p.raster : 1;
+    const int block = t / (raster * p.n_tiles), m0 = block * raster;
+    const int high = min(raster, num_m - m0), in = t - m0 * p.n_tiles;
+    const int nt = in / high;
+    return make_int2(m0 + in - nt * high, nt);
+}
+
+// Row tile mt of the launch: {expert, first activation row, valid rows, first permuted row}.
 template <int kMode>
 __device__ __forceinline__ int4 tile_of(const Int8Gemm& p, int mt, int rows) {
     if (kMode != kDense) return __ldg(p.tiles + mt);
@@ -239,12 +250,13 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
             if (p.early) {
                 int kb = 0;
                 for (int t = pair; t < total_tiles && pre < kStages;) {
-                    const int4 ti = tile_of<kMode>(p, t / p.n_tiles, rows);
+                    const int2 at = place_of<kMode>(p, num_m, t);
+                    const int4 ti = tile_of<kMode>(p, at.x, rows);
                     if (leader) {
                         mbar_arrive_expect_tx(&bars->full[pre], stage_bytes(ti.z));
                         last_phase[pre] = 0;
                     }
-                    weights(pre, ti.x, t % p.n_tiles * kPairM + 128 * (int)rank, kb);
+                    weights(pre, ti.x, at.y * kPairM + 128 * (int)rank, kb);
                     ++pre;
                     if (++kb == kb_count) {
                         kb = 0;
@@ -253,11 +265,14 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
                 }
                 pdl_wait();
             }
-            int4 ti_n = total_tiles > pair ? tile_of<kMode>(p, pair / p.n_tiles, rows) : make_int4(0, 0, 0, 0);
+            auto tile_at = [&](int t) {
+                return t < total_tiles ? tile_of<kMode>(p, place_of<kMode>(p, num_m, t).x, rows) : make_int4(0, 0, 0, 0);
+            };
+            int4 ti_n = tile_at(pair);
             for (int t = pair; t < total_tiles && ok; t += npairs) {
-                const int mt = t / p.n_tiles, nt = t - mt * p.n_tiles;
+                const int nt = place_of<kMode>(p, num_m, t).y;
                 const int4 ti = ti_n;
-                if (t + npairs < total_tiles) ti_n = tile_of<kMode>(p, (t + npairs) / p.n_tiles, rows);
+                ti_n = tile_at(t + npairs);
                 const int hb = tile_n(ti.z) >> 1;
                 const uint32_t tx = stage_bytes(ti.z);
                 const CUtensorMap* mb = &tmB->m[(hb >> 4) - 1];
@@ -314,12 +329,15 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
             bool ok = true;
             int it = 0;
             // rows of the next tile, fetched ahead
-            int zn = total_tiles > pair ? tile_of<kMode>(p, pair / p.n_tiles, rows).z : 0;
+            auto rows_at = [&](int t) {
+                return t < total_tiles ? tile_of<kMode>(p, place_of<kMode>(p, num_m, t).x, rows).z : 0;
+            };
+            int zn = rows_at(pair);
             for (int t = pair; t < total_tiles && ok; t += npairs, ++it) {
                 const int buf = it & 1;
                 const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
                 const int n = tile_n(zn);
-                if (t + npairs < total_tiles) zn = tile_of<kMode>(p, (t + npairs) / p.n_tiles, rows).z;
+                zn = rows_at(t + npairs);
                 const uint32_t idesc = idesc_i8(kPairM, n);
                 const uint32_t b_atom16 = (uint32_t)(n >> 1) * 8u;  // one atom of this CTA's rows, in 16 bytes
                 if (!mbar_wait_bounded(&bars->acc_empty[buf], acc_phase ^ 1u, abort_flag, p.wait_limit_ns)) {
@@ -377,10 +395,10 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
                                         map_to_cta(smem_u32(&bars->acc_empty[1]), 0)};
         float* s_xs = reinterpret_cast<float*>(sEpi + (size_t)(warp - 2) * kEpiBytes);
         auto first_row = [&](int t) {  // this warp's first weight row in tile t
-            return (t % p.n_tiles) * kPairM + 128 * (int)rank + 32 * quad;
+            return place_of<kMode>(p, num_m, t).y * kPairM + 128 * (int)rank + 32 * quad;
         };
         auto tile_at = [&](int t) {
-            return t < total_tiles ? tile_of<kMode>(p, t / p.n_tiles, rows) : make_int4(0, 0, 0, 0);
+            return t < total_tiles ? tile_of<kMode>(p, place_of<kMode>(p, num_m, t).x, rows) : make_int4(0, 0, 0, 0);
         };
         float xs_next[4], ws_next = 0.0f;
         auto fetch = [&](int t, int4 ti) {  // scales of tile t: lane l holds its rows l, l + 32, ... of this warp

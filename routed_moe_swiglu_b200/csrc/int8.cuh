@@ -128,6 +128,7 @@ struct Int8Gemm {
     const int* live;                // null: all rows
     int rows;
     int out_bf16;
+    int raster;                     // row tiles of a block of tiles (dense)
     int early;                      // launched by a kernel that waited before it released this one
 };
 
