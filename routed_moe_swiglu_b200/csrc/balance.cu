@@ -567,7 +567,7 @@ __device__ __forceinline__ void finish_total(const BalanceArgs& a, FinishShared&
     if (threadIdx.x == 0) {
         const float zt = total > 0 ? a.z_coef / (float)total : 0.0f;
         a.losses[0] = loss;
-        a.losses[1] = total > 0 ? zt * z : 0.0f;
+        a.losses[1] = zt != 0.0f ? zt * z : 0.0f;  // without a z loss, 0 even where lse^2 overflows
         a.grad_scales[S] = 2.0f * zt;
     }
 }

@@ -261,6 +261,7 @@ bool row_map(CUtensorMap* map, const void* base, long long rows, int cols, long 
 bool few_is_faster(const Int8Gemm& g, int cols_in) {
     const double sms = num_sms(), K = cols_in;
     const long long rows = g.rows;
+    if (rows > 128ll * 65535) return false;  // row tiles are a grid's second dimension
     const double wide_n = rows < kRouteTile ? (double)((rows + 31) / 32 * 32) : (double)kRouteTile;
     const long long wide = (rows + kRouteTile - 1) / kRouteTile * g.n_tiles;
     const double waves = (double)((wide + (long long)(sms / 2) - 1) / (long long)(sms / 2));

@@ -144,7 +144,9 @@ def _check(r, ref, coef, zc, chosen=True):
     # the balance loss: positive terms, a product and a sum over E more than the sums
     assert abs(got[0] - ref["losses"][0]) <= (P_ERR + terms + 64) * U * ref["losses"][0]
     total = max(int(ref["n"].sum()), 1)
-    if zc:
+    if not zc:
+        assert got[1] == 0
+    else:
         z_err = zc / total * (2 * np.abs(ref["lse"][al]) * lse_err + terms * U * ref["lse"][al] ** 2).sum()
         assert abs(got[1] - ref["losses"][1]) <= z_err + 4 * U * abs(ref["losses"][1])
     d = r.dlogits.cpu().double().numpy()
