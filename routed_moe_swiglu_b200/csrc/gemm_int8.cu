@@ -12,7 +12,7 @@
 // its N operand (a multiple of 32 up to 256), so that an expert's last tile and
 // a short batch cost their own row count, as in the bf16 kernels:
 //   gate/up  256 rows of W1 (gate and up interleaved in groups of 16, so that
-//            the warp reading a TMEM quarter holds both of 16 f) -> SwiGLU ->
+//            a thread reads both of an f from its TMEM quarter) -> SwiGLU ->
 //            bf16 h rows, quantised by a pass of their own (a row's scale needs
 //            all of F)
 //   down     256 rows of W2 -> fp32 y rows
@@ -26,6 +26,17 @@
 // CTA 0, issues the MMAs; warps 2-17 drain two accumulators of 256 columns.
 // Every mbarrier wait is bounded; the pair meets in cluster barriers only at
 // start-up and before TMEM is released.
+//
+// What bounds it (B200).  Dense, 8192^3: 350 us cold and 370-405 sustained, 2.7 to
+// 3.1 POP/s, where twice the measured bf16 rate is 3.3: the power limit lowers the
+// clock.  65,536 routes of 128 experts, H 2,048, F 1,024: gate/up 247 us (2.2
+// POP/s), down 178 us.  Without epilogues they take 210 and 78: gate/up is bound by
+// what an SM takes in from L2 (88 bytes a nanosecond), as its 320 row tiles hold 205
+// rows on average and each loads all of its weights; down by the stores of its fp32
+// y rows, 537 MB, 91 us alone.
+// 256 tokens of the same experts (16 rows each): 92 us and 51 us for 537 and 268 MB
+// of weights, 5.8 and 5.2 TB/s of the measured 6.5; a launch's first loads and last
+// tile, ten us together, are what is missing.
 #include "int8.cuh"
 #include "ptx.cuh"
 
@@ -129,6 +140,45 @@ __device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)
         : "r"(taddr)
         : "memory");
 }
+// Threads 0-15 read 8 columns of 16 TMEM lanes from taddr, threads 16-31 the next 8 of the same lanes.
+__device__ __forceinline__ void tmem_ld_16x32bx2_x8(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x32bx2.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8], 8;"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr)
+        : "memory");
+}
+// Two fp32 products or sums in one instruction, each rounded as alone.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+// sigmoid_approx of two.
+__device__ __forceinline__ float2 sigmoid_approx2(float2 g) {
+    float2 e = mul2(g, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    e = add2(e, make_float2(1.0f, 1.0f));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+    asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+    return e;
+}
+// float(a) * xs * ws of two sums.
+__device__ __forceinline__ float2 scaled2(uint32_t a0, uint32_t a1, float2 xs, float2 ws) {
+    return mul2(mul2(make_float2(__int2float_rn((int)a0), __int2float_rn((int)a1)), xs), ws);
+}
 __device__ __forceinline__ void store_as(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_as(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 // The lane's values of n rows, ld apart; of the first `left` of them only.
@@ -173,7 +223,7 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&bars->acc_full[b], 1);
-            mbar_init(&bars->acc_empty[b], 2 * kEpiWarps * (kMode == kDown ? 1 : kEpiGroups));
+            mbar_init(&bars->acc_empty[b], 2 * kEpiWarps);  // (of a tile that both groups share nobody waits for it)
         }
         mbar_init(&bars->done, 1);
         bars->abort_flag = 0;
@@ -377,17 +427,17 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
         }
         __syncwarp();
     } else {
-        // ---------------- epilogue: warps 2..17, in two groups of eight.  The down GEMM, whose stores
-        // take longest, gives the groups the pair's tiles in turn (one accumulator each); the others
-        // share each tile among both, which frees its accumulator sooner (65,536 routes: gate/up 297 us
-        // shared, 309 in turn; down 178 and 174).  A pair with one tile at most always shares it.
+        // ---------------- epilogue: warps 2..17, in two groups of eight, which take the pair's tiles in
+        // turn, one accumulator each: a group's loads and stores wait while the other's run (65,536
+        // routes: gate/up 294 us, 298 where both share each tile; down 178 and 181).  A pair with one
+        // tile at most shares it.
         // TMEM lanes are weight rows (output
         // columns), TMEM columns activation rows: a lane's weight scale is a register, a row's scale
         // comes from shared memory, and the 32 lanes' stores of one row are neighbours.  The next
         // tile's scales are fetched while this one is drained.
         const int ew = (warp - 2) & (kEpiWarps - 1), group = (warp - 2) / kEpiWarps;
         const int quad = warp & 3;  // TMEM lane quarter this warp may read
-        const bool share = kMode != kDown || total_tiles <= npairs;
+        const bool share = total_tiles <= npairs;
         // this warp takes the chunks c = c0, c0 + cs, ... of kChunk columns
         const int c0 = (ew >> 2) + (share ? 2 * group : 0), cs = share ? 4 : 2;
         const int step = share ? npairs : kEpiGroups * npairs;
@@ -440,10 +490,21 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
             const uint32_t taddr = tmem_base + ((uint32_t)(quad * 32) << 16) + (uint32_t)buf * kAccCols;
             const int f0 = p.relu2 ? w0 : w0 >> 1;  // gate/up: first of this warp's 32 (16) f
             const bool cols = (kMode == kGateUp ? f0 : w0) < p.out_cols;
+            const bool glu = kMode == kGateUp && !p.relu2;
+            const float ws_gate = glu ? __shfl_sync(0xffffffffu, ws, lane & 15) : 0.0f;
+            const float ws_up = glu ? __shfl_sync(0xffffffffu, ws, 16 + (lane & 15)) : 0.0f;
 #pragma unroll 1
             for (int c = c0, i = 0; c < nch; c += cs, ++i) {
+                // SwiGLU: lanes < 16 take the chunk's first eight rows, the others its last, of gate (the
+                // quarter's first 16 TMEM lanes) and of up (its last 16) alike
+                constexpr int kHalf = kChunk / 2;
                 uint32_t v[kChunk];
-                tmem_ld_32x32b_x16(taddr + c * kChunk, v);
+                if (glu) {
+                    tmem_ld_16x32bx2_x8(taddr + c * kChunk, v);
+                    tmem_ld_16x32bx2_x8(taddr + (16u << 16) + c * kChunk, v + kHalf);
+                } else {
+                    tmem_ld_32x32b_x16(taddr + c * kChunk, v);
+                }
                 float pv = 1.0f;  // gate/up with probabilities: lane l holds row l's
                 if (kMode == kGateUp && p.route_probs != nullptr && c * kChunk + (lane & 15) < ti.z)
                     pv = __ldg(p.route_probs + __ldg(p.perm + ti.w + c * kChunk + (lane & 15)));
@@ -454,52 +515,62 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
                     if (lane == 0) mbar_arrive_cluster_relaxed(acc_empty0[buf]);
                 }
                 if (!cols) continue;
+                // rows of this chunk that exist; a whole chunk is stored without asking row by row
+                // (branches around each store cost a quarter of the epilogue's time)
+                const int left = ti.z - c * kChunk;
+                __nv_bfloat16* h = kMode == kGateUp ? reinterpret_cast<__nv_bfloat16*>(p.out) +
+                                                          (size_t)(ti.y + c * kChunk) * (size_t)p.out_ld + f0
+                                                    : nullptr;
+                if (glu) {
+                    // silu(g) * u = g * u / (1 + exp(-g))
+                    const int r0 = lane < 16 ? 0 : kHalf;
+                    const float4* xs4 = reinterpret_cast<const float4*>(s_xs + i * kChunk + r0);
+                    float hv[kHalf];
+#pragma unroll
+                    for (int q = 0; q < kHalf / 2; ++q) {
+                        const float4 x4 = xs4[q >> 1];
+                        const float2 xs = q & 1 ? make_float2(x4.z, x4.w) : make_float2(x4.x, x4.y);
+                        float2 gt = scaled2(v[2 * q], v[2 * q + 1], xs, make_float2(ws_gate, ws_gate));
+                        float2 up = scaled2(v[kHalf + 2 * q], v[kHalf + 2 * q + 1], xs, make_float2(ws_up, ws_up));
+                        if (p.clamp > 0.0f) {
+                            gt = make_float2(clamp_nan(gt.x, p.clamp), clamp_nan(gt.y, p.clamp));
+                            up = make_float2(clamp_nan(up.x, p.clamp), clamp_nan(up.y, p.clamp));
+                        }
+                        float2 o = mul2(mul2(gt, up), sigmoid_approx2(gt));
+                        if (p.route_probs != nullptr)
+                            o = mul2(o, make_float2(__shfl_sync(0xffffffffu, pv, r0 + 2 * q),
+                                                    __shfl_sync(0xffffffffu, pv, r0 + 2 * q + 1)));
+                        hv[2 * q] = o.x;
+                        hv[2 * q + 1] = o.y;
+                    }
+                    store_rows<kHalf>(h + (size_t)r0 * (size_t)p.out_ld + (lane & 15), p.out_ld, hv,
+                                      left >= kChunk ? kHalf : left - r0);
+                    continue;
+                }
                 const float4* xs4 = reinterpret_cast<const float4*>(s_xs + i * kChunk);
                 float g[kChunk];
 #pragma unroll
                 for (int q = 0; q < kChunk / 4; ++q) {
                     const float4 xs = xs4[q];
-                    g[4 * q] = __int2float_rn((int)v[4 * q]) * xs.x * ws;
-                    g[4 * q + 1] = __int2float_rn((int)v[4 * q + 1]) * xs.y * ws;
-                    g[4 * q + 2] = __int2float_rn((int)v[4 * q + 2]) * xs.z * ws;
-                    g[4 * q + 3] = __int2float_rn((int)v[4 * q + 3]) * xs.w * ws;
+                    const float2 a = scaled2(v[4 * q], v[4 * q + 1], make_float2(xs.x, xs.y), make_float2(ws, ws));
+                    const float2 b = scaled2(v[4 * q + 2], v[4 * q + 3], make_float2(xs.z, xs.w), make_float2(ws, ws));
+                    g[4 * q] = a.x;
+                    g[4 * q + 1] = a.y;
+                    g[4 * q + 2] = b.x;
+                    g[4 * q + 3] = b.y;
                 }
-                // rows of this chunk that exist; a whole chunk is stored without asking row by row
-                // (branches around each store cost a quarter of the epilogue's time)
-                const int left = ti.z - c * kChunk;
                 if (kMode == kGateUp) {
-                    __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(p.out) +
-                                       (size_t)(ti.y + c * kChunk) * (size_t)p.out_ld + f0;
                     if (p.clamp > 0.0f) {
 #pragma unroll
                         for (int j = 0; j < kChunk; ++j) g[j] = clamp_nan(g[j], p.clamp);
                     }
-                    if (p.relu2) {
 #pragma unroll
-                        for (int j = 0; j < kChunk; ++j) {
-                            const float r = g[j] > 0.0f || g[j] != g[j] ? g[j] : 0.0f;  // a NaN row stays NaN
-                            g[j] = r * r;
-                            if (p.route_probs != nullptr) g[j] *= __shfl_sync(0xffffffffu, pv, j);
-                        }
-                        store_rows<kChunk>(h + lane, p.out_ld, g, left);
-                    } else {
-                        // lanes < 16 hold gate, the others up of the same f: lanes < 16 keep the chunk's
-                        // first rows and receive their up values, the others keep its last rows and
-                        // receive gate.  silu(g) * u = g * u / (1 + exp(-g)): the product needs no order
-                        constexpr int kHalf = kChunk / 2;
-                        const bool lo = lane < 16;
-                        const int r0 = lo ? 0 : kHalf;
-                        float hv[kHalf];
-#pragma unroll
-                        for (int j = 0; j < kHalf; ++j) {
-                            const float mine = lo ? g[j] : g[kHalf + j];
-                            const float other = __shfl_xor_sync(0xffffffffu, lo ? g[kHalf + j] : g[j], 16);
-                            hv[j] = mine * other * sigmoid_approx(lo ? mine : other);
-                            if (p.route_probs != nullptr) hv[j] *= __shfl_sync(0xffffffffu, pv, r0 + j);
-                        }
-                        store_rows<kHalf>(h + (size_t)r0 * (size_t)p.out_ld + (lane & 15), p.out_ld, hv,
-                                          left >= kChunk ? kHalf : left - r0);
+                    for (int j = 0; j < kChunk; ++j) {
+                        const float r = g[j] > 0.0f || g[j] != g[j] ? g[j] : 0.0f;  // a NaN row stays NaN
+                        g[j] = r * r;
+                        if (p.route_probs != nullptr) g[j] *= __shfl_sync(0xffffffffu, pv, j);
                     }
+                    store_rows<kChunk>(h + lane, p.out_ld, g, left);
                 } else if (w0 + lane < p.out_cols) {
                     const size_t at = (size_t)(ti.y + c * kChunk) * (size_t)p.out_ld + w0 + lane;
                     if (kMode == kDense && p.out_bf16 != 0)
