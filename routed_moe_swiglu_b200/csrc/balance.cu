@@ -27,6 +27,17 @@
 // same bits every run.  Long runs of a sequence are shared by the block's warps;
 // runs of a few tokens are a warp's own.  The rows come through a ring in shared
 // memory that each lane fills for itself (cp.async), two rows ahead.
+//
+// What bounds it (B200).  Both launches read the logits once and the gradient
+// writes them once; with 65,536 tokens x 128 experts, k 8, 16 sequences (74 MB of
+// memory traffic, 11 us at the copy rate) the losses take 18.9 us, 5.5 of them the
+// finishing kernel, and the gradient 18.6, where a plain copy of the same 34 MB
+// takes 11.8: what is above the copy is instructions (an exponential and eight
+// operations a value, two shuffles a token and route), which register rows and the
+// ring leave in the open when the rows arrive from L2.  Short batches are bound by
+// the chain of launches and meetings: 64 tokens x 8 experts, one cluster and one
+// launch, 6.6 us and the gradient 3.2; 4,099 x 128 in seven sequences 11.5 and 4.5;
+// 3,001 x 1,000 15 and 10.
 #include <cmath>
 
 #include "moe_internal.cuh"
@@ -40,7 +51,7 @@ constexpr int kBalWarps = kBalThreads / 32;
 constexpr int kBalSumRows = kBalWarps / 2;  // rows of sums in shared memory: half of the warps add the other half's
 template <int V>
 constexpr int kRingOf = V <= 16 ? 3 : 2;    // rows of a lane group in flight or in use
-constexpr int kShortPasses = 4;             // a sequence's run of so many passes of a warp is that warp's alone
+constexpr int kShortPasses = 4;             // a sequence's run of so many passes of a warp is that warp's alone (8: slower)
 constexpr int kGradThreads = 256;
 constexpr int kGradWarps = kGradThreads / 32;
 template <int V>

@@ -6,6 +6,10 @@
 // and walks the token's rows, so that d_t is read once for all of them.  The
 // dot products are sums of 128 threads' partial sums in fp32, added in a fixed
 // order whatever the number of routes a block takes.
+//
+// Bound by memory: y is read and dy written once.  8,192 tokens x 8 routes x
+// 2,048: 186 us for 1.14 GB, 6.1 TB/s, 0.94 of the measured copy rate; 333 x 6 x
+// 2,688 with bf16 gradients: 10.7 us for 45 MB, where start and end count.
 #include "moe_internal.cuh"
 
 namespace moe {
@@ -83,7 +87,7 @@ __device__ __forceinline__ void walk(const CombineGradArgs& a, int t, int c, int
 
 // Items are (token, group of its routes).  With fewer live tokens than `fill` the k routes are spread
 // over several blocks, each reading d_t again (from L2) for its own rows.  With more, a block for
-// each token leaves the SMs no uneven last round (8,192 tokens x 8 x 2,048: 178 us, against 200 with
+// each token leaves the SMs no uneven last round (8,192 tokens x 8 x 2,048: 186 us, against 200 with
 // eight blocks an SM that walk the tokens).
 // kMost: the most routes a token may have, 8 or 16.
 template <bool kBf16, int kMost>

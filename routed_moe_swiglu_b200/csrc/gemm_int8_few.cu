@@ -16,6 +16,10 @@
 // (tcgen05 kind::i8, M = 128), warps 2-5 quantise (kFused) and drain.  Every
 // mbarrier wait is bounded; a wait that gave up is followed by the same cluster
 // barriers as any other, so no CTA is left alone in one.
+//
+// One token, 2048 -> 4096: 5.95 us, where reading the weights takes 1.3: launch,
+// cluster start, quantising, one chain of loads, the exchange of partial sums and
+// the end, about a microsecond each.  As two launches of the wide kernels 8.8 us.
 #include "int8.cuh"
 #include "ptx.cuh"
 

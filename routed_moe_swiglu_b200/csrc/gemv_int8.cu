@@ -15,6 +15,11 @@
 //   down     eight output columns of bf16 h rows -> fp32 y rows
 // The sums are exact and what follows is the wide kernels' arithmetic: the same
 // bits.
+//
+// One token, six experts of H 2,688, F 1,856 (90 MB of weights, 13.7 us at the
+// copy rate): the whole forward takes 32.0 us, 42.8 on the wide kernels; 10 us of
+// it are the permute's and the combine's launches.  Eight tokens an expert would
+// cost 96-115 us against 77: hence the limit of four.
 #include "int8.cuh"
 
 namespace moe {
