@@ -205,7 +205,8 @@ moe_status nvfp4_quantize_block16(const void* in, long long rows, int cols, long
  * product with it is NaN.  in bf16 [rows, ld_in]; q int8 [rows, cols], scales
  * fp32 [rows]; live_rows_dev as for mxfp8_quantize_block32.  cols a positive
  * multiple of 8, ld_in >= cols and a multiple of 8, `in` 16-byte aligned, q
- * 8-byte aligned. */
+ * 8-byte aligned.  rows may be 0: nothing is done, and the rows' pointers may be
+ * NULL (as an empty tensor's are). */
 moe_status int8_quantize_rows(const void* in, long long rows, int cols, long long ld_in, int8_t* q, float* scales,
                               const int* live_rows_dev, void* stream);
 
@@ -221,7 +222,8 @@ moe_status int8_quantize_rows(const void* in, long long rows, int cols, long lon
  *   status_dev: nullable device word that MOE_DEV_TIMEOUT is or-ed into should a
  *   bounded on-device wait give up (the outputs are then not valid).
  * cols_in: a multiple of 16 up to MOE_INT8_MAX_K; cols_out up to 2^20; rows up to
- * 2^24; ld_x >= cols_in and a multiple of 16; x and w 16-byte aligned.  A row's
+ * 2^24 (0: nothing is done, and the rows' pointers may be NULL); ld_x >= cols_in
+ * and a multiple of 16; x and w 16-byte aligned.  A row's
  * results do not depend on the other rows or on the live count.  Enqueues work
  * only. */
 #define MOE_INT8_MAX_K 131056

@@ -17,8 +17,8 @@
 // bits.
 //
 // One token, six experts of H 2,688, F 1,856 (90 MB of weights, 13.7 us at the
-// copy rate): the whole forward takes 32.0 us, 42.8 on the wide kernels; 10 us of
-// it are the permute's and the combine's launches.  Eight tokens an expert would
+// copy rate): the whole forward takes 29.2 us, 42.8 on the wide kernels; 13 us of
+// it are five launches' (32.2 with a warp a row where a block's codes are computed).  Eight tokens an expert would
 // cost 96-115 us against 77: hence the limit of four.
 #include "int8.cuh"
 
@@ -52,6 +52,7 @@ template <bool kGateUp, int kTokens>
 __global__ void __launch_bounds__(kGvThreads) moe_gemv_int8_kernel(const GemvArgs a) {
     extern __shared__ __align__(16) uint8_t s_codes[];  // [tokens][atoms * 128]
     __shared__ float s_xs[kGvTokens];
+    __shared__ uint32_t s_red[kGvWarps];
     const Int8Gemm& p = a.g;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int pitch = p.atoms * 128;
@@ -99,21 +100,15 @@ __global__ void __launch_bounds__(kGvThreads) moe_gemv_int8_kernel(const GemvArg
     }
     if (nt <= 0) return;
 
-    // codes of the tokens' rows: a warp a row
-    const int chunks = a.cols_in / 8;
-    for (int r = warp; r < nt; r += kGvWarps) {
-        const long long at = kGateUp ? __ldg(p.perm + ti.w + r) / a.top_k : ti.y + r;
-        const uint4* src = a.x + (size_t)at * a.ld_x;
-        uint32_t m = 0u;
-#pragma unroll 4
-        for (int c = lane; c < chunks; c += 32) m = int8_amax_pairs(__ldg(src + c), m);
-        const Int8Row row = int8_row(__uint_as_float(__reduce_max_sync(0xffffffffu, int8_amax_bits(m))));
-        uint2* dst = reinterpret_cast<uint2*>(s_codes + (size_t)r * pitch);
-#pragma unroll 4
-        for (int c = lane; c < chunks; c += 32) dst[c] = int8_codes8(__ldg(src + c), row);
-        // past the row the weights' codes are 0, and what stands here is of no account
-        if (lane == 0) s_xs[r] = row.scale;
-    }
+    // codes of the tokens' rows, the block's warps spread over them (past a row the weights' codes are
+    // 0, and what stands in shared memory is of no account)
+    constexpr int kRowWarps = kGvWarps / kTokens;
+    const int r = warp / kRowWarps;
+    const long long at = r >= nt ? 0 : kGateUp ? __ldg(p.perm + ti.w + r) / a.top_k : ti.y + r;
+    const float scale = int8_quantize_row<kRowWarps, 4>(
+        a.x + (size_t)at * a.ld_x, a.cols_in / 8, r < nt, s_red, [] {},
+        [&](int c, uint2 codes) { reinterpret_cast<uint2*>(s_codes + (size_t)r * pitch)[c] = codes; });
+    if (r < nt && (threadIdx.x & (kRowWarps * 32 - 1)) == 0) s_xs[r] = scale;
     __syncthreads();
     if (!work) return;
 

@@ -25,52 +25,6 @@ constexpr int kI8Threads = 128;
 // twice.
 constexpr int kMostHeld = 8;
 
-template <int kWarps>
-__device__ __forceinline__ uint32_t row_max(uint32_t a, uint32_t* s_red) {
-    a = __reduce_max_sync(0xffffffffu, a);
-    if (kWarps > 1) {
-        const int warp = threadIdx.x >> 5;
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) s_red[warp] = a;
-        __syncthreads();
-        const int w0 = warp / kWarps * kWarps;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) a = max(a, s_red[w0 + w]);
-    }
-    return a;
-}
-
-// Quantises the row of `chunks` 16-byte chunks at src (none when !on): store(c, codes) for each
-// chunk, after ready(); returns the scale.  Every thread of the row's warps calls it (with kWarps
-// > 1, of the block).
-template <int kWarps, int kHeld, class Ready, class Store>
-__device__ __forceinline__ float quantize_row(const uint4* src, int chunks, bool on, uint32_t* s_red, Ready ready,
-                                              Store store) {
-    constexpr int kLanes = kWarps * 32;
-    const int lane = threadIdx.x & (kLanes - 1);
-    uint4 v[kHeld];
-    uint32_t a = 0u;
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int c = i * kLanes + lane;
-        v[i] = on && c < chunks ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-    }
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) a = int8_amax_pairs(v[i], a);
-    if (on)
-        for (int c = kHeld * kLanes + lane; c < chunks; c += kLanes) a = int8_amax_pairs(__ldg(src + c), a);
-    const Int8Row row = int8_row(__uint_as_float(row_max<kWarps>(int8_amax_bits(a), s_red)));
-    ready();
-#pragma unroll
-    for (int i = 0; i < kHeld; ++i) {
-        const int c = i * kLanes + lane;
-        if (on && c < chunks) store(c, int8_codes8(v[i], row));
-    }
-    if (on)
-        for (int c = kHeld * kLanes + lane; c < chunks; c += kLanes) store(c, int8_codes8(__ldg(src + c), row));
-    return row.scale;
-}
-
 // Rows of bf16, kWarps warps a row.
 template <int kWarps, int kHeld>
 __global__ void __launch_bounds__(kI8Threads, kHeld > 4 ? 6 : 10) int8_quantize_rows_kernel(const uint4* __restrict__ in, long long rows,
@@ -90,7 +44,7 @@ __global__ void __launch_bounds__(kI8Threads, kHeld > 4 ? 6 : 10) int8_quantize_
     for (long long r0 = (long long)blockIdx.x * kRows; r0 < n; r0 += (long long)gridDim.x * kRows) {
         const long long r = r0 + threadIdx.x / (kWarps * 32);
         const bool on = r < n;
-        const float s = quantize_row<kWarps, kHeld>(in + r * ld_chunks, chunks, on, s_red, [] {},
+        const float s = int8_quantize_row<kWarps, kHeld>(in + r * ld_chunks, chunks, on, s_red, [] {},
                                                     [&](int c, uint2 codes) { q[r * chunks + c] = codes; });
         if (on && (threadIdx.x & (kWarps * 32 - 1)) == 0) scales[r] = s;
     }
@@ -134,7 +88,7 @@ __global__ void __launch_bounds__(kI8Threads) gather_rows_int8_kernel(const uint
                 if (pr >= 0) xq[(size_t)pr * chunks_out + c] = codes;
             }
         };
-        const float s = quantize_row<kI8Threads / 32, kHeld>(x + (size_t)t * chunks, chunks, true, s_red, ready, put);
+        const float s = int8_quantize_row<kI8Threads / 32, kHeld>(x + (size_t)t * chunks, chunks, true, s_red, ready, put);
         if (threadIdx.x < k && s_prow[threadIdx.x] >= 0) xs[s_prow[threadIdx.x]] = s;
         for (int c = chunks + threadIdx.x; c < chunks_out; c += kI8Threads) put(c, make_uint2(0u, 0u));
     }
@@ -158,7 +112,7 @@ __global__ void __launch_bounds__(kI8Threads, kHeld > 4 ? 6 : 10) quantize_h_int
     for (long long i0 = (long long)blockIdx.x * kRows; i0 < n; i0 += (long long)gridDim.x * kRows) {
         const long long i = i0 + threadIdx.x / (kWarps * 32);
         const int pr = i < n ? __ldg(inv + i) : -1;
-        const float s = quantize_row<kWarps, kHeld>(h + (size_t)(pr < 0 ? 0 : pr) * chunks, chunks, pr >= 0, s_red,
+        const float s = int8_quantize_row<kWarps, kHeld>(h + (size_t)(pr < 0 ? 0 : pr) * chunks, chunks, pr >= 0, s_red,
                                                     [] {}, [&](int c, uint2 codes) { hq[(size_t)pr * chunks + c] = codes; });
         if (pr >= 0 && (threadIdx.x & (kWarps * 32 - 1)) == 0) hs[pr] = s;
     }
@@ -193,7 +147,7 @@ __global__ void __launch_bounds__(kI8Threads) prepare_int8_kernel(
         const int chunks = (first ? H : F) / 8, atoms = first ? at1 : at2, per = first ? w1r : hr;
         const long long grow = e * per + wrow;
         uint2* dst = (first ? w1q : w2q) + ((size_t)(grow >> 7) * atoms * 128 + (grow & 127)) * 16;
-        const float s = quantize_row<kI8Threads / 32, kMostHeld>(src, chunks, true, s_red, [] {}, [&](int c, uint2 codes) {
+        const float s = int8_quantize_row<kI8Threads / 32, kMostHeld>(src, chunks, true, s_red, [] {}, [&](int c, uint2 codes) {
             dst[(size_t)(c >> 4) * (128 * 16) + (c & 15)] = codes;
         });
         if (threadIdx.x == 0) (first ? w1s : w2s)[grow] = s;
@@ -213,7 +167,7 @@ constexpr int kMaxColsI8 = 1 << 20;
 // Checks that int8_matmul and int8_linear share (the activations apart).
 moe_status check_product(long long rows, int cols_in, const void* w, const float* w_scales, int cols_out,
                          const void* out, long long ld_out) {
-    if (w == nullptr || w_scales == nullptr || out == nullptr) return MOE_ERR_INVALID_ARG;
+    if (w == nullptr || w_scales == nullptr || (rows != 0 && out == nullptr)) return MOE_ERR_INVALID_ARG;
     if (rows < 0 || cols_in <= 0 || cols_out <= 0 || ld_out < cols_out) return MOE_ERR_INVALID_ARG;
     // 131,071 products of -128 * -128 fill an int32 sum
     if (cols_in % 16 != 0 || cols_in > MOE_INT8_MAX_K || cols_out > kMaxColsI8 || rows > kMaxRowsI8)
@@ -373,7 +327,7 @@ extern "C" {
 
 moe_status int8_quantize_rows(const void* in, long long rows, int cols, long long ld_in, int8_t* q, float* scales,
                               const int* live_rows_dev, void* stream) {
-    if (in == nullptr || q == nullptr || scales == nullptr) return MOE_ERR_INVALID_ARG;
+    if (rows != 0 && (in == nullptr || q == nullptr || scales == nullptr)) return MOE_ERR_INVALID_ARG;
     if (rows < 0 || cols <= 0 || ld_in < cols) return MOE_ERR_INVALID_ARG;
     if (cols % 8 != 0) return MOE_ERR_UNSUPPORTED;
     if (ld_in % 8 != 0 || !is_aligned(in, 16) || !is_aligned(q, 8) || !is_aligned(scales, 4)) return MOE_ERR_ALIGNMENT;
@@ -386,7 +340,7 @@ moe_status int8_quantize_rows(const void* in, long long rows, int cols, long lon
 moe_status int8_matmul(const int8_t* x, const float* x_scales, long long rows, int cols_in, long long ld_x,
                        const int8_t* w, const float* w_scales, int cols_out, void* out, long long ld_out,
                        int out_bf16, const int* live_rows_dev, unsigned* status_dev, void* stream) {
-    if (x == nullptr || x_scales == nullptr || ld_x < cols_in) return MOE_ERR_INVALID_ARG;
+    if ((rows != 0 && (x == nullptr || x_scales == nullptr)) || ld_x < cols_in) return MOE_ERR_INVALID_ARG;
     const moe_status st = check_product(rows, cols_in, w, w_scales, cols_out, out, ld_out);
     if (st != MOE_OK) return st;
     if (ld_x % 16 != 0 || !is_aligned(x, 16) || !is_aligned(x_scales, 4) || !is_aligned(out, out_bf16 ? 2 : 4))
@@ -406,7 +360,7 @@ moe_status int8_linear(const void* x, long long rows, int cols_in, long long ld_
                        const float* w_scales, int cols_out, void* out, long long ld_out, int out_bf16,
                        const int* live_rows_dev, void* workspace, size_t ws_bytes, unsigned* status_dev,
                        void* stream) {
-    if (x == nullptr || workspace == nullptr || ld_x < cols_in) return MOE_ERR_INVALID_ARG;
+    if ((rows != 0 && x == nullptr) || workspace == nullptr || ld_x < cols_in) return MOE_ERR_INVALID_ARG;
     const moe_status st = check_product(rows, cols_in, w, w_scales, cols_out, out, ld_out);
     if (st != MOE_OK) return st;
     if (ws_bytes < int8_linear_workspace_bytes(rows, cols_in)) return MOE_ERR_WORKSPACE_TOO_SMALL;

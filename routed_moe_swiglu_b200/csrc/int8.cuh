@@ -91,6 +91,53 @@ __device__ __forceinline__ uint32_t int8_amax_pairs(uint4 v, uint32_t a) {
 // The larger of a pair, as the bits of an fp32.
 __device__ __forceinline__ uint32_t int8_amax_bits(uint32_t a) { return max(a << 16, a & 0xffff0000u); }
 
+// The largest of a row's kWarps warps (s_red: a word a warp of the block).
+template <int kWarps>
+__device__ __forceinline__ uint32_t int8_row_max(uint32_t a, uint32_t* s_red) {
+    a = __reduce_max_sync(0xffffffffu, a);
+    if (kWarps > 1) {
+        const int warp = threadIdx.x >> 5;
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) s_red[warp] = a;
+        __syncthreads();
+        const int w0 = warp / kWarps * kWarps;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) a = max(a, s_red[w0 + w]);
+    }
+    return a;
+}
+
+// Quantises the row of `chunks` 16-byte chunks at src (none when !on): store(c, codes) for each
+// chunk, after ready(); returns the scale.  Every thread of the row's warps calls it (with kWarps
+// > 1, of the block).
+template <int kWarps, int kHeld, class Ready, class Store>
+__device__ __forceinline__ float int8_quantize_row(const uint4* src, int chunks, bool on, uint32_t* s_red, Ready ready,
+                                                   Store store) {
+    constexpr int kLanes = kWarps * 32;
+    const int lane = threadIdx.x & (kLanes - 1);
+    uint4 v[kHeld];
+    uint32_t a = 0u;
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int c = i * kLanes + lane;
+        v[i] = on && c < chunks ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) a = int8_amax_pairs(v[i], a);
+    if (on)
+        for (int c = kHeld * kLanes + lane; c < chunks; c += kLanes) a = int8_amax_pairs(__ldg(src + c), a);
+    const Int8Row row = int8_row(__uint_as_float(int8_row_max<kWarps>(int8_amax_bits(a), s_red)));
+    ready();
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) {
+        const int c = i * kLanes + lane;
+        if (on && c < chunks) store(c, int8_codes8(v[i], row));
+    }
+    if (on)
+        for (int c = kHeld * kLanes + lane; c < chunks; c += kLanes) store(c, int8_codes8(__ldg(src + c), row));
+    return row.scale;
+}
+
 // x clamped to [-c, c]; a NaN (a row that holds one) stays NaN.
 __device__ __forceinline__ float clamp_nan(float x, float c) {
     float r;

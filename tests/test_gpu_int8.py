@@ -275,6 +275,18 @@ def test_weights_written_just_before():
         _same(out, product_ref(*quantize_ref(x), *quantize_ref(w), False))
 
 
+def test_no_rows():
+    x, w, ws = torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(32, 64, dtype=torch.int8, device="cuda"), \
+        torch.ones(32, device="cuda")
+    q, s, out = torch.zeros(0, 64, dtype=torch.int8, device="cuda"), torch.zeros(0, device="cuda"), torch.zeros(0, 32, device="cuda")
+    buf = torch.zeros(rm.int8_linear_workspace_bytes(0, 64), dtype=torch.uint8, device="cuda")
+    rm.int8_quantize_rows(x, q, s)
+    rm.int8_matmul(q, s, w, ws, out)
+    rm.int8_linear(x, w, ws, out, buf)
+    rm.int8_linear(x[:0], w, ws, out, buf)
+    torch.cuda.synchronize()
+
+
 def test_two_streams():
     g = torch.Generator().manual_seed(12)
     jobs = []

@@ -70,6 +70,18 @@ def test_products_reject_bad_arguments():
     assert rm.int8_linear_workspace_bytes(100, 256) >= 100 * 260
 
 
+def test_no_rows():
+    """An empty tensor's pointer is null: with no rows the rows' pointers are not asked for."""
+    lib = rm.load_library()
+    assert lib.int8_quantize_rows(None, 0, 64, 64, None, None, None, None) == 0
+    assert lib.int8_matmul(None, None, 0, 64, 64, F, F, 32, None, 32, 0, None, None, None) == 0
+    assert lib.int8_linear(None, 0, 64, 64, F, F, 32, None, 32, 1, None, F, 256, None, None) == 0
+    # what does not belong to the rows is
+    assert lib.int8_matmul(None, None, 0, 64, 64, None, F, 32, None, 32, 0, None, None, None) == 1
+    assert lib.int8_linear(None, 0, 64, 64, F, F, 32, None, 32, 1, None, None, 256, None, None) == 1
+    assert lib.int8_quantize_rows(None, 0, 60, 64, None, None, None, None) == 2
+
+
 def test_the_binding_refuses_other_types_and_shapes():
     i8, bf = torch.int8, torch.bfloat16
     x, q, s = torch.zeros(4, 64, dtype=bf), torch.zeros(4, 64, dtype=i8), torch.zeros(4)
