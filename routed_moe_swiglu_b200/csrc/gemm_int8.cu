@@ -29,7 +29,7 @@
 //
 // What bounds it (B200).  Dense, 8192^3: 350 us cold and 370-405 sustained, 2.7 to
 // 3.1 POP/s, where twice the measured bf16 rate is 3.3: the power limit lowers the
-// clock.  65,536 routes of 128 experts, H 2,048, F 1,024: gate/up 247 us (2.2
+// clock.  65,536 routes of 128 experts, H 2,048, F 1,024: gate/up 245 us (2.2
 // POP/s), down 178 us.  Without epilogues they take 210 and 78: gate/up is bound by
 // what an SM takes in from L2 (88 bytes a nanosecond), as its 320 row tiles hold 205
 // rows on average and each loads all of its weights; down by the stores of its fp32
@@ -429,7 +429,7 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
     } else {
         // ---------------- epilogue: warps 2..17, in two groups of eight, which take the pair's tiles in
         // turn, one accumulator each: a group's loads and stores wait while the other's run (65,536
-        // routes: gate/up 294 us, 298 where both share each tile; down 178 and 181).  A pair with one
+        // routes: gate/up with the pass over h 294 us, 298 where both share each tile; down 178 and 181).  A pair with one
         // tile at most shares it.
         // TMEM lanes are weight rows (output
         // columns), TMEM columns activation rows: a lane's weight scale is a register, a row's scale
