@@ -429,12 +429,11 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
     } else {
         // ---------------- epilogue: warps 2..17, in two groups of eight, which take the pair's tiles in
         // turn, one accumulator each: a group's loads and stores wait while the other's run (65,536
-        // routes: gate/up with the pass over h 294 us, 298 where both share each tile; down 178 and 181).  A pair with one
-        // tile at most shares it.
-        // TMEM lanes are weight rows (output
-        // columns), TMEM columns activation rows: a lane's weight scale is a register, a row's scale
-        // comes from shared memory, and the 32 lanes' stores of one row are neighbours.  The next
-        // tile's scales are fetched while this one is drained.
+        // routes: gate/up with the pass over h 294 us, 298 where both share each tile; down 178 and
+        // 181).  A pair with one tile at most shares it.  TMEM lanes are weight rows (output columns),
+        // TMEM columns activation rows: a lane's weight scale is a register, a row's scale comes from
+        // shared memory, and the 32 lanes' stores of one row are neighbours.  The next tile's scales
+        // are fetched while this one is drained.
         const int ew = (warp - 2) & (kEpiWarps - 1), group = (warp - 2) / kEpiWarps;
         const int quad = warp & 3;  // TMEM lane quarter this warp may read
         const bool share = total_tiles <= npairs;
