@@ -3,7 +3,8 @@
 A thin ctypes binding over the C ABI of ``libroutedmoe.so`` (declared in
 ``include/moe.h``).  Every function here only marshals arguments: torch
 tensors become device pointers, the current torch CUDA stream becomes the
-``stream`` argument.  All computation runs in the library's CUDA kernels;
+``stream`` argument (for the operators with the shortest calls a compiled
+binding does that, where it is built).  All computation runs in the library's CUDA kernels;
 there is no CPU path, and calling any entry point without the built library
 raises.
 
@@ -133,7 +134,30 @@ def load_library():
         fn.argtypes = args
         fn.restype = res
     _lib = lib
+    _load_short(lib)
     return lib
+
+
+# The compiled binding's functions of the operators whose calls are shorter than reading their
+# arguments here (csrc/binding.cpp).  They do nothing and return None wherever an argument is not
+# as it should be, and the call goes the long way below; None: not built, or no such torch.
+_short = None
+
+
+def _load_short(lib) -> None:
+    global _short
+    import torch
+
+    api = getattr(torch.Tensor, "__dlpack_c_exchange_api__", None)
+    try:
+        from . import _binding
+    except ImportError:
+        return
+    entries = ("cudaGetDevice", "moe_plan_get_desc", "moe_balance_loss", "moe_route_backward", "moe_combine_backward",
+               "int8_quantize_rows", "int8_matmul", "int8_linear")
+    if api is not None and _binding.start(api, torch.Tensor, torch.nn.Parameter,
+                                          *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in entries)):
+        _short = _binding
 
 
 def _status_string(code: int) -> str:
@@ -196,6 +220,7 @@ class Plan:
 
     def __init__(self, handle, desc: _Desc):
         self._h = handle
+        self._addr = handle.value or 0
         self.hidden = desc.hidden
         self.ffn = desc.ffn
         self.num_experts = desc.num_experts
@@ -217,6 +242,7 @@ class Plan:
         if self._h is not None and _lib is not None:
             _lib.moe_plan_destroy(self._h)
         self._h = None
+        self._addr = 0
 
     def __del__(self):
         try:
@@ -303,6 +329,10 @@ MOE_INT8_MAX_K = 131056
 def int8_quantize_rows(x, q, scales, live_rows=None, stream=None) -> None:
     """x bf16 [rows, cols] (row stride in elements a multiple of 8) -> q int8 [rows, cols] with a scale
     for each row, scales fp32 [rows] (include/moe.h)."""
+    if _short is not None:
+        code = _short.int8_quantize_rows(None if stream is None else _stream(stream), x, q, scales, live_rows)
+        if code is not None:
+            return _check(code, "int8_quantize_rows")
     import torch
 
     _strided("x", x, torch.bfloat16)
@@ -347,6 +377,11 @@ def _int8_operands(x, wq, w_scales, out, live_rows, status) -> int:
 def int8_matmul(xq, x_scales, wq, w_scales, out, live_rows=None, status=None, stream=None) -> None:
     """out[t, c] = sum_k xq[t, k] * wq[c, k] * x_scales[t] * w_scales[c]: xq int8 [rows, K] (row stride a
     multiple of 16), wq int8 [N, K], out fp32 or bf16 [rows, N] (include/moe.h)."""
+    if _short is not None:
+        code = _short.int8_matmul(None if stream is None else _stream(stream), xq, x_scales, wq, w_scales, out, live_rows,
+                                  status)
+        if code is not None:
+            return _check(code, "int8_matmul")
     import torch
 
     _strided("xq", xq, torch.int8)
@@ -365,6 +400,11 @@ def int8_linear_workspace_bytes(rows: int, cols_in: int) -> int:
 def int8_linear(x, wq, w_scales, out, workspace, live_rows=None, status=None, stream=None) -> None:
     """int8_matmul of bf16 rows x [rows, K] (row stride a multiple of 8), quantised in the call;
     workspace: int8_linear_workspace_bytes(rows, K) bytes."""
+    if _short is not None:
+        code = _short.int8_linear(None if stream is None else _stream(stream), x, workspace, wq, w_scales, out, live_rows,
+                                  status)
+        if code is not None:
+            return _check(code, "int8_linear")
     import torch
 
     _strided("x", x, torch.bfloat16)
@@ -416,6 +456,12 @@ def moe_balance_loss(plan: Plan, logits, ids, live_count, counts, prob_sums, lse
     """The router's balance and z losses with per-expert counts (include/moe.h).  The number of
     sequences is counts.shape[0]; outputs: counts int32 and prob_sums fp32 [num_seqs, E], lse fp32
     [capacity], losses fp32 [2] (balance, z), grad_scales fp32 [num_seqs + 1] (for moe_route_backward)."""
+    if _short is not None:
+        code = _short.moe_balance_loss(None if stream is None else _stream(stream), plan._addr, logits, ids, live_count,
+                                       counts, prob_sums, lse, losses, grad_scales, workspace, balance_coef, z_coef,
+                                       token_mask, seq_offsets)
+        if code is not None:
+            return _check(code, "moe_balance_loss")
     import torch
 
     f32, i32 = torch.float32, torch.int32
@@ -442,6 +488,11 @@ def moe_route_backward(plan: Plan, logits, ids, live_count, dlogits, lse=None, c
     """Gradient of the router's logits (include/moe.h): the losses' part from logits, lse, counts and
     grad_scales (as moe_balance_loss left them) and grad_losses fp32 [2] (None: 1, 1); the chosen
     part from ids, probs and dprobs.  Either part may be None."""
+    if _short is not None:
+        code = _short.moe_route_backward(None if stream is None else _stream(stream), plan._addr, logits, ids, live_count,
+                                         dlogits, lse, counts, grad_scales, grad_losses, probs, dprobs, seq_offsets)
+        if code is not None:
+            return _check(code, "moe_route_backward")
     import torch
 
     f32, i32 = torch.float32, torch.int32
@@ -470,6 +521,11 @@ def moe_combine_backward(plan: Plan, dout, y_rows, route_rows, route_probs, live
                          stream=None) -> None:
     """Gradient of the combine (include/moe.h): dprobs[t, j] = <dout[t], y_rows[route_rows[t, j]]> and
     dy_rows[route_rows[t, j]] = route_probs[t, j] * dout[t]; either may be None."""
+    if _short is not None:
+        code = _short.moe_combine_backward(None if stream is None else _stream(stream), plan._addr, dout, y_rows,
+                                           route_rows, route_probs, live_count, dprobs, dy_rows)
+        if code is not None:
+            return _check(code, "moe_combine_backward")
     import torch
 
     f32, i32 = torch.float32, torch.int32

@@ -1,4 +1,5 @@
-"""Build the CUDA library libroutedmoe.so in-tree with nvcc for sm_100a.
+"""Build the CUDA library libroutedmoe.so in-tree with nvcc for sm_100a, and
+_binding.so, the short way from Python into it, with the C++ compiler.
 
     python -m routed_moe_swiglu_b200.build [--force]
 
@@ -15,12 +16,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libroutedmoe.so")
+BINDING = os.path.join(PKG, "_binding.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + os.path.join(ROOT, "include"),
@@ -52,6 +55,21 @@ def _compile(src, extra, verbose):
     return obj
 
 
+def _build_binding(force, verbose):
+    src, include = os.path.join(CSRC, "binding.cpp"), sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        print(f"no {include}/Python.h: _binding.so is not built, short calls go through ctypes", file=sys.stderr)
+        return
+    if force or _stale(BINDING, [src] + _headers() + [__file__]):
+        tmp = BINDING + ".tmp"
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + include,
+               "-I" + os.path.join(ROOT, "include"), src, "-o", tmp]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.check_call(cmd)
+        os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     if force:
@@ -68,6 +86,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             print(" ".join(cmd), flush=True)
         subprocess.check_call(cmd)
         os.replace(tmp, LIB)
+    _build_binding(force, verbose)
     return LIB
 
 

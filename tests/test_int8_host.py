@@ -97,3 +97,15 @@ def test_the_binding_refuses_other_types_and_shapes():
                 lambda: rm.int8_linear(q, w, ws, out, buf), lambda: rm.int8_linear(x, w.float(), ws, out, buf)):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_the_compiled_binding_leaves_host_tensors_alone():
+    rm.load_library()
+    if rm._short is None:
+        pytest.skip("the compiled binding is not built, or this torch has no exchange table")
+    x, q, s = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4)
+    for args in ((None, x, q, s, None), (None, None, None, None, None), (None, "x", 1, object(), None), (None, x, q, s),
+                 (), ("stream", x, q, s, None)):
+        assert rm._short.int8_quantize_rows(*args) is None
+    assert rm._short.moe_combine_backward(None, 0, s, s, s, s, s, s, s) is None
+    assert rm._short.start(*[None] * 11) is False and rm._short.start() is False
