@@ -24,19 +24,19 @@
 // sequence s) pair it meets writes its sums to slot b + s.  Blocks and
 // sequences both advance along the tokens, so no two pairs share a slot, and a
 // finishing step adds a sequence's slots in block order: no float atomics, the
-// same bits every run.  Long runs of a sequence are shared by the block's warps;
-// runs of a few tokens are a warp's own.  The rows come through a ring in shared
+// same bits every run.  The warps of a block share the runs it meets, all at once:
+// long ones in segments, short ones whole.  The rows come through a ring in shared
 // memory that each lane fills for itself (cp.async), two rows ahead.
 //
 // What bounds it (B200).  Both launches read the logits once and the gradient
 // writes them once; with 65,536 tokens x 128 experts, k 8, 16 sequences (74 MB of
-// memory traffic, 11 us at the copy rate) the losses take 18.9 us, 5.5 of them the
+// memory traffic, 11 us at the copy rate) the losses take 18.3 us, 5.5 of them the
 // finishing kernel, and the gradient 18.6, where a plain copy of the same 34 MB
 // takes 11.8: what is above the copy is instructions (an exponential and eight
 // operations a value, two shuffles a token and route), which register rows and the
 // ring leave in the open when the rows arrive from L2.  Short batches are bound by
 // the chain of launches and meetings: 64 tokens x 8 experts, one cluster and one
-// launch, 6.6 us and the gradient 3.2; 4,099 x 128 in seven sequences 11.5 and 4.5;
+// launch, 6.6 us and the gradient 3.2; 4,099 x 128 in seven sequences 10.6 and 4.5;
 // 3,001 x 1,000 15 and 10.
 #include <cmath>
 
@@ -48,10 +48,9 @@ namespace {
 
 constexpr int kBalThreads = 512;
 constexpr int kBalWarps = kBalThreads / 32;
-constexpr int kBalSumRows = kBalWarps / 2;  // rows of sums in shared memory: half of the warps add the other half's
+constexpr int kCutRuns = kBalWarps / 2;     // runs of a block that can be shared by warps
 template <int V>
 constexpr int kRingOf = V <= 16 ? 3 : 2;    // rows of a lane group in flight or in use
-constexpr int kShortPasses = 4;             // a sequence's run of so many passes of a warp is that warp's alone (8: slower)
 constexpr int kGradThreads = 256;
 constexpr int kGradWarps = kGradThreads / 32;
 template <int V>
@@ -327,7 +326,6 @@ __device__ __forceinline__ void balance_stats(const BalanceArgs& a, int n, float
     const int E = a.E;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, gl = lane & (L - 1);
     constexpr int kGroups = 32 / L;  // tokens a warp holds at once
-    constexpr int kShort = kShortPasses * kGroups;
     const int chunk = (n + a.blocks - 1) / a.blocks;
     const int c0 = min(n, (int)blockIdx.x * chunk), c1 = min(n, c0 + chunk);
     if (c0 >= c1) return;
@@ -336,97 +334,166 @@ __device__ __forceinline__ void balance_stats(const BalanceArgs& a, int n, float
     for (int t = c0 + threadIdx.x; t < c1; t += kBalThreads)
         if (t < first || t >= last) a.lse[t] = -INFINITY;
 
-    // The runs of this block: of each sequence, [t_lo, t_hi).  First the short ones, a warp each in
-    // turn, then the long ones, all warps together.
+    // The runs of this block: of each sequence it meets, its tokens [lo, hi) here.  Runs of more than
+    // `most` tokens are cut into segments of so many, one a warp (`most` is the least that leaves a
+    // warp one segment or run, but at most twice what the tokens alone ask for); a shorter run is a
+    // warp's own.  So all runs are read at once: 512 tokens of 1,000 experts in 16 sequences take
+    // 14.6 us, 19.6 run after run, each with its own start.
     const int s0 = find_seq_warp(a.seq_off, a.num_seqs, c0);
-    int runs = 0, longs = 0;
-    for (int s = s0; s < a.num_seqs; ++s) {
-        const int sb = seq_begin(a.seq_off, s, n);
-        if (sb >= c1) break;
-        const int t_lo = max(sb, c0), t_hi = min(seq_begin(a.seq_off, s + 1, n), c1);
-        if (t_lo >= t_hi) continue;
-        if (t_hi - t_lo > kShort) {
-            ++longs;
-            continue;
+    if (s0 >= a.num_seqs) return;
+    struct Run {
+        int lo, hi;
+        __device__ int len() const { return hi > lo ? hi - lo : 0; }
+    };
+    auto run_of = [&](int s) {  // in the sweeps lane l's, of sequence s
+        if (s >= a.num_seqs) return Run{c1, c1};
+        return Run{max(seq_begin(a.seq_off, s, n), c0), min(seq_begin(a.seq_off, s + 1, n), c1)};
+    };
+    auto ends = [&](int base) { return base + 32 >= a.num_seqs || seq_begin(a.seq_off, base + 32, n) >= c1; };
+    int passes = (c1 - c0 + kBalWarps * kGroups - 1) / (kBalWarps * kGroups);
+    const Run whole = run_of(s0);
+    const bool alone = whole.hi >= c1 || s0 + 1 == a.num_seqs;  // no other run
+    if (!alone) {
+        if (ends(s0)) {
+            const int len = run_of(s0 + lane).len();
+            for (const int least = passes; passes < 2 * least; ++passes) {
+                const int most = passes * kGroups;
+                if (__reduce_add_sync(0xffffffffu, (len + most - 1) / most) <= kBalWarps) break;
+            }
+        } else {
+            passes *= 2;  // always enough
         }
-        if (runs++ % kBalWarps != warp) continue;
-        const size_t slot = (size_t)blockIdx.x + s;
-        float acc[V], z = 0.0f;
-        int cnt = 0;
+    }
+    const int most = passes * kGroups;
+    auto segments = [&](const Run& r) { return r.len() > most ? (r.len() + most - 1) / most : 0; };
+    // f(base, the lane's run, its segments, the first of them, cut runs before base) for every 32
+    // sequences; returns the segments
+    auto sweep = [&](auto f) {
+        int total = 0, runs = 0;
+        for (int base = s0;; base += 32) {
+            const Run r = run_of(base + lane);
+            const int m = segments(r);
+            int sum = m;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int below = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += below;
+            }
+            f(base, r, m, total + sum - m, runs);
+            runs += __popc(__ballot_sync(0xffffffffu, m > 0));
+            total += __shfl_sync(0xffffffffu, sum, 31);
+            if (ends(base)) return total;
+        }
+    };
+    // this warp's segment, and the row of its run's counts (at least two segments each, but for a run
+    // alone: at most kCutRuns rows)
+    int seg_lo = 0, seg_hi = 0, row = 0, cut;
+    int step = kGroups;
+    if (alone) {  // every warp in turn
+        cut = min(kBalWarps, (whole.len() + kGroups - 1) / kGroups);
+        step = kBalWarps * kGroups;
+        seg_lo = whole.lo + warp * kGroups;
+        seg_hi = whole.hi;
+    } else {
+        cut = sweep([&](int, const Run& r, int m, int first, int runs) {
+            const unsigned cuts = __ballot_sync(0xffffffffu, m > 0);
+            const unsigned mine = __ballot_sync(0xffffffffu, first <= warp && warp < first + m);
+            if (mine != 0u) {
+                const int from = __ffs(mine) - 1;
+                seg_lo = __shfl_sync(0xffffffffu, r.lo, from) + (warp - __shfl_sync(0xffffffffu, first, from)) * most;
+                seg_hi = min(seg_lo + most, __shfl_sync(0xffffffffu, r.hi, from));
+                row = runs + __popc(cuts & ((1u << from) - 1u));
+            }
+        });
+    }
+    if (cut > 0) {
+        for (int e = threadIdx.x; e < (alone ? 1 : kCutRuns) * E; e += kBalThreads) s_cnt[e] = 0;
+        __syncthreads();
+    }
+    float acc[V], z = 0.0f;
+    int cnt = 0;
+    auto clear = [&] {
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-        int* counts = a.slot_c + slot * E;
-        for (int e = lane; e < E; e += 32) counts[e] = 0;
-        __syncwarp();
-        sum_tokens<L, V, kVec>(a, ring, t_lo, t_hi, kGroups, acc, z, cnt, [&](int id) { atomicAdd(counts + id, 1); });
+        z = 0.0f;
+        cnt = 0;
+    };
+    auto leave = [&](float* to) {  // the warp's sums
         if (lane < L)
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int c = col_of<L, kVec>(v, gl);
-                if (c < E) a.slot_p[slot * E + c] = acc[v];
+                if (c < E) to[c] = acc[v];
             }
-        if (lane == 0) {
-            a.slot_z[slot] = z;
-            a.slot_n[slot] = cnt;
-        }
-    }
-    if (longs == 0) return;
-    for (int s = s0; s < a.num_seqs; ++s) {
-        const int sb = seq_begin(a.seq_off, s, n);
-        if (sb >= c1) break;
-        const int t_lo = max(sb, c0), t_hi = min(seq_begin(a.seq_off, s + 1, n), c1);
-        if (t_hi - t_lo <= kShort) continue;
-        for (int e = threadIdx.x; e < E; e += kBalThreads) s_cnt[e] = 0;
-        __syncthreads();
-        float acc[V], z = 0.0f;
-        int cnt = 0;
-#pragma unroll
-        for (int v = 0; v < V; ++v) acc[v] = 0.0f;
-        sum_tokens<L, V, kVec>(a, ring, t_lo + warp * kGroups, t_hi, kBalWarps * kGroups, acc, z, cnt,
-                               [&](int id) { atomicAdd(&s_cnt[id], 1); });  // integers: any order
+    };
+    if (seg_lo < seg_hi) {
+        int* counts = s_cnt + row * E;
+        clear();
+        sum_tokens<L, V, kVec>(a, ring, seg_lo, seg_hi, step, acc, z, cnt,
+                               [&](int id) { atomicAdd(counts + id, 1); });  // integers: any order
+        leave(s_sum + warp * E);
         if (lane == 0) {
             sh.z[warp] = z;
             sh.n[warp] = cnt;
         }
-        // the warps in order: the upper half's rows first go through shared memory to the lower
-        // half, which adds them and leaves its rows there
-        float* mine = s_sum + (warp & (kBalSumRows - 1)) * E;
-        if (warp >= kBalSumRows && lane < L)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = col_of<L, kVec>(v, gl);
-                if (c < E) mine[c] = acc[v];
+    }
+    // the i-th short run is warp (cut + i) % kBalWarps's
+    for (int base = s0, shorts = 0; !alone; base += 32) {
+        const Run r = run_of(base + lane);
+        const bool is = r.len() > 0 && segments(r) == 0;
+        const unsigned all = __ballot_sync(0xffffffffu, is);
+        const int at = cut + shorts + __popc(all & ((1u << lane) - 1u));
+        shorts += __popc(all);
+        for (unsigned left = __ballot_sync(0xffffffffu, is && at % kBalWarps == warp); left != 0u; left &= left - 1) {
+            const int from = __ffs(left) - 1;
+            const size_t slot = (size_t)blockIdx.x + base + from;
+            int* counts = a.slot_c + slot * E;
+            for (int e = lane; e < E; e += 32) counts[e] = 0;
+            __syncwarp();
+            clear();
+            sum_tokens<L, V, kVec>(a, ring, __shfl_sync(0xffffffffu, r.lo, from), __shfl_sync(0xffffffffu, r.hi, from),
+                                   kGroups, acc, z, cnt, [&](int id) { atomicAdd(counts + id, 1); });
+            leave(a.slot_p + slot * E);
+            if (lane == 0) {
+                a.slot_z[slot] = z;
+                a.slot_n[slot] = cnt;
             }
-        __syncthreads();
-        if (warp < kBalSumRows && lane < L)
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const int c = col_of<L, kVec>(v, gl);
-                if (c < E) mine[c] += acc[v];
-            }
-        __syncthreads();
+        }
+        if (ends(base)) break;
+    }
+    if (cut == 0) return;
+    // the segments of each cut run, in order
+    __syncthreads();
+    auto join = [&](int s, int w0, int w1, const int* counts) {
         const size_t slot = (size_t)blockIdx.x + s;
         for (int e = threadIdx.x; e < E; e += kBalThreads) {
             float p = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kBalSumRows; ++w) p += s_sum[w * E + e];
+            for (int w = 0; w < kBalWarps; ++w) p += w >= w0 && w < w1 ? s_sum[w * E + e] : 0.0f;
             a.slot_p[slot * E + e] = p;
-            a.slot_c[slot * E + e] = s_cnt[e];
+            a.slot_c[slot * E + e] = counts[e];
         }
         if (threadIdx.x == 0) {
             float zs = 0.0f;
             int ns = 0;
 #pragma unroll
             for (int w = 0; w < kBalWarps; ++w) {
-                zs += sh.z[w];
-                ns += sh.n[w];
+                zs += w >= w0 && w < w1 ? sh.z[w] : 0.0f;
+                ns += w >= w0 && w < w1 ? sh.n[w] : 0;
             }
             a.slot_z[slot] = zs;
             a.slot_n[slot] = ns;
         }
-        if (--longs == 0) break;
-        __syncthreads();
-    }
+    };
+    if (alone)
+        join(s0, 0, cut, s_cnt);
+    else
+        sweep([&](int base, const Run&, int m, int first, int runs) {
+            for (unsigned cuts = __ballot_sync(0xffffffffu, m > 0); cuts != 0u; cuts &= cuts - 1, ++runs) {
+                const int from = __ffs(cuts) - 1, w0 = __shfl_sync(0xffffffffu, first, from);
+                join(base + from, w0, w0 + __shfl_sync(0xffffffffu, m, from), s_cnt + runs * E);
+            }
+        });
 }
 
 // Adds the slots of sequence s for 32 experts: an item is one (sequence, 32 experts) of the
@@ -587,7 +654,7 @@ __device__ __forceinline__ void finish_total(const BalanceArgs& a, FinishShared&
 // the totals; else balance_finish_kernel does the rest.
 template <int L, int V, bool kVec, bool kOne>
 __global__ void __launch_bounds__(kBalThreads, 1) balance_stats_kernel(const BalanceArgs a) {
-    extern __shared__ __align__(16) float s_bal[];  // the warps' rings, [kBalSumRows][E] sums, [E] counts
+    extern __shared__ __align__(16) float s_bal[];  // the warps' rings, [kBalWarps][E] sums, [kCutRuns][E] counts
     __shared__ StatsShared sh;
     pdl_wait();
     pdl_trigger();  // after the wait: the finishing kernel reads sizes and offsets before its own
@@ -596,9 +663,10 @@ __global__ void __launch_bounds__(kBalThreads, 1) balance_stats_kernel(const Bal
     constexpr int kRingFloats = kRingOf<V> * 32 * V;  // of a warp
     float* s_sum = s_bal + kBalWarps * kRingFloats;
     balance_stats<L, V, kVec>(a, n, s_bal + (threadIdx.x >> 5) * kRingFloats, s_sum,
-                              reinterpret_cast<int*>(s_sum + kBalSumRows * a.E), sh);
+                              reinterpret_cast<int*>(s_sum + kBalWarps * a.E), sh);
     if constexpr (kOne) {
-        __shared__ FinishShared fin;
+        static_assert(sizeof(FinishShared) <= kBalWarps * kRingFloats * 4, "the finish takes the rings' place");
+        FinishShared& fin = *reinterpret_cast<FinishShared*>(s_bal);
         cluster_sync();  // the slots of every block are written
         finish_items<1>(a, n, blockIdx.x, gridDim.x, fin);
         cluster_sync();
@@ -895,21 +963,20 @@ cudaError_t launch_cluster(void (*kern)(KArgs...), int blocks, int threads, size
 
 template <int L, int V, bool kVec>
 struct LaunchStats {
-    static constexpr size_t smem(int E) {
-        return (size_t)(kBalWarps * kRingOf<V> * 32 * V + (kBalSumRows + 1) * E) * 4;
+    static constexpr size_t smem(int E, bool one_seq) {  // of a sequence alone no block meets two
+        return (size_t)(kBalWarps * kRingOf<V> * 32 * V + (kBalWarps + (one_seq ? 1 : kCutRuns)) * E) * 4;
     }
     static cudaError_t go(const BalanceArgs& a, cudaStream_t s) {
-        static_assert(smem(L * V) + sizeof(FinishShared) + sizeof(StatsShared) + 1024 <= 232448, "shared memory budget");
+        static_assert(smem(L * V, false) + sizeof(StatsShared) + 1024 <= 232448, "shared memory budget");
         static bool done[2][64];
         const bool one = a.blocks <= kClusterBlocks;
-        const size_t most = smem(L * V);
+        const size_t most = smem(L * V, false), need = smem(a.E, a.num_seqs == 1);
         cudaError_t err = one ? allow_smem(balance_stats_kernel<L, V, kVec, true>, most, done[1])
                               : allow_smem(balance_stats_kernel<L, V, kVec, false>, most, done[0]);
         if (err != cudaSuccess) return err;
         if (one)
-            return launch_cluster(balance_stats_kernel<L, V, kVec, true>, a.blocks, kBalThreads, smem(a.E), s, a);
-        return launch_dependent(balance_stats_kernel<L, V, kVec, false>, dim3(a.blocks), dim3(kBalThreads), smem(a.E), s,
-                                a);
+            return launch_cluster(balance_stats_kernel<L, V, kVec, true>, a.blocks, kBalThreads, need, s, a);
+        return launch_dependent(balance_stats_kernel<L, V, kVec, false>, dim3(a.blocks), dim3(kBalThreads), need, s, a);
     }
 };
 template <int L, int V, bool kVec>

@@ -200,6 +200,21 @@ def test_sequences_that_are_empty_or_leave_tokens_out():
         _check(r, _reference(q, 0.3, 0.1), 0.3, 0.1)
 
 
+@pytest.mark.parametrize("T,E,k,offsets", [
+    (700, 128, 8, [3, 641]), (700, 128, 8, [690, 700]), (70, 1000, 16, [10, 12]), (70, 1000, 16, [5, 5]),
+    (3000, 64, 4, [0, 1, 2, 3, 1500, 1501, 2999]), (513, 1024, 8, [0, 500, 503, 505, 513]),
+    (900, 16, 2, list(range(0, 200)) + [500, 900]), (257, 257, 3, [0, 100, 100, 130, 200, 257]),
+    (300, 8, 1, [0, 17, 34, 51, 68, 85, 102, 119, 136, 153, 170, 187, 204, 300])])
+def test_runs_of_every_kind(T, E, k, offsets):
+    """Blocks that meet one sequence, some, or many; long ones cut into segments beside short ones;
+    tokens before the first and behind the last."""
+    q = _problem(T, E, k, len(offsets) - 1, seed=T + E, masked=True, offsets=offsets)
+    r = _Run(q)
+    r.forward(0.3, 0.02)
+    r.backward()
+    _check(r, _reference(q, 0.3, 0.02), 0.3, 0.02)
+
+
 def test_rows_that_nothing_is_left_of():
     """Masked rows may hold anything; a row of -infinity does not count; -infinity and the type's lowest
     value disable experts; ids outside the experts are dropped; a mask of zeros leaves losses of 0."""
