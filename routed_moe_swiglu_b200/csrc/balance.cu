@@ -878,11 +878,15 @@ constexpr int kClusterBlocks = 8;
 // The workspace has rows for the largest grid any device may ask for.
 constexpr int kMaxBalBlocks = 256;
 
-// Blocks of the sums: one pass of each block's warps at least, `cap` at most.
-int balance_blocks(long long max_live, int E, long long cap) {
+// Blocks of the sums: one pass of each block's warps at least, `cap` at most; in one cluster as many
+// as give each item of the finish a warp (117 tokens of 16 experts in 64 sequences: 9.2 us, 16.8 with
+// the one block that the tokens need).
+int balance_blocks(long long max_live, int E, int num_seqs, long long cap) {
     const int b = blocks_for(max_live, kBalWarps * tokens_per_warp(E), cap);
     if (b > kClusterBlocks) return b;
-    return b > 4 ? 8 : b > 2 ? 4 : b;
+    const long long items = (long long)num_seqs * ((E + kFinCols - 1) / kFinCols);
+    const int f = blocks_for(items, kBalWarps, kClusterBlocks), w = b > f ? b : f;
+    return w > 4 ? 8 : w > 2 ? 4 : w;
 }
 
 struct BalanceLayout {
@@ -890,7 +894,7 @@ struct BalanceLayout {
 };
 BalanceLayout balance_layout(const moe_plan* plan, int num_seqs) {
     const size_t E = (size_t)plan->d.num_experts, S = (size_t)num_seqs;
-    const int b = balance_blocks(plan->max_live, plan->d.num_experts, kMaxBalBlocks);
+    const int b = balance_blocks(plan->max_live, plan->d.num_experts, num_seqs, kMaxBalBlocks);
     const size_t slots = (size_t)b + S;
     BalanceLayout l;
     size_t off = 0;
@@ -1028,7 +1032,7 @@ moe_status moe_balance_loss(const moe_plan* plan, const float* logits, const int
     a.E = plan->d.num_experts;
     a.k = plan->d.top_k;
     a.num_seqs = num_seqs;
-    a.blocks = balance_blocks(plan->max_live, a.E, num_sms() < kMaxBalBlocks ? num_sms() : kMaxBalBlocks);
+    a.blocks = balance_blocks(plan->max_live, a.E, num_seqs, num_sms() < kMaxBalBlocks ? num_sms() : kMaxBalBlocks);
     a.balance_coef = balance_coef;
     a.z_coef = z_coef;
     a.counts = counts;

@@ -17,6 +17,8 @@ namespace {
 
 constexpr int kCgThreads = 128;
 constexpr int kCgWarps = kCgThreads / 32;
+constexpr int kLaneChunks = 4;  // of a short row, a lane's 16-byte chunks at most
+constexpr int kJ = 4;           // of a short row's token, routes at a time
 
 struct CombineGradArgs {
     const void* dout;
@@ -147,6 +149,97 @@ __global__ void __launch_bounds__(kCgThreads, kMost > 8 ? 5 : 7) combine_backwar
     }
 }
 
+// Short rows (H <= 4 * kLaneChunks * 32): L lanes hold d_t, at most kLaneChunks 16-byte chunks each, and
+// walk the token's rows four at a time; 32 / L tokens a warp.  A block a token would leave most of its
+// threads without a chunk (46,692 tokens x 1 x 80: 10.2 us, 87 with a block a token).
+template <bool kBf16, int L>
+__global__ void __launch_bounds__(kCgThreads, 5) combine_backward_short_kernel(const CombineGradArgs a) {
+    pdl_trigger();
+    pdl_wait();
+    const int n = clamp_live(a.live, a.max_live), k = a.k, chunks = a.H / 4;
+    const int gl = threadIdx.x & (L - 1);
+    const long long step = (long long)gridDim.x * (kCgThreads / L);
+    // items: a token, or with few of them kJ of its routes
+    const int batches = (k + kJ - 1) / kJ;
+    const int split = (long long)n * batches <= step ? batches : 1;
+    // every lane of a warp goes round as often as its first group
+    for (long long i0 = (long long)blockIdx.x * (kCgThreads / L) + (threadIdx.x & ~31) / L; i0 < (long long)n * split;
+         i0 += step) {
+        const long long item = i0 + (threadIdx.x & 31) / L, t = item / split;
+        const bool on = t < n;
+        const int j_lo = (int)(item - t * split) * kJ;
+        float4 d[kLaneChunks];
+#pragma unroll
+        for (int u = 0; u < kLaneChunks; ++u) {
+            const int c = gl + u * L;
+            d[u] = on && c < chunks ? load_grad<kBf16>(a.dout, (size_t)t * chunks + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        // the token's rows and probabilities, a route a lane (k <= 16: two with L = 8)
+        int row[2] = {-1, -1};
+        float pr[2] = {0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            if (on && gl + i * L < k && (i == 0 || L < kMaxTopK)) {
+                row[i] = __ldg(a.rows + t * k + gl + i * L);
+                pr[i] = __ldg(a.probs + t * k + gl + i * L);
+            }
+        for (int j0 = j_lo, i = 0; i < (split > 1 ? 1 : batches); ++i, j0 += kJ) {
+            int r[kJ];
+            float p[kJ];
+            float4 v[kJ][kLaneChunks];
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+                const int at = j0 + j;
+                const bool second = at >= L;
+                r[j] = __shfl_sync(0xffffffffu, second ? row[1] : row[0], at & (L - 1), L);
+                p[j] = __shfl_sync(0xffffffffu, second ? pr[1] : pr[0], at & (L - 1), L);
+                if (at >= k) r[j] = -1;
+            }
+            if (a.dprobs != nullptr) {
+#pragma unroll
+                for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                    for (int u = 0; u < kLaneChunks; ++u) {
+                        const int c = gl + u * L;
+                        v[j][u] = r[j] >= 0 && c < chunks ? __ldg(a.y + (size_t)r[j] * chunks + c)
+                                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                    }
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) {
+                    float x = 0.0f;
+#pragma unroll
+                    for (int u = 0; u < kLaneChunks; ++u)
+                        x = fmaf(d[u].w, v[j][u].w, fmaf(d[u].z, v[j][u].z, fmaf(d[u].y, v[j][u].y, fmaf(d[u].x, v[j][u].x, x))));
+#pragma unroll
+                    for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+                    // a route without a row has no gradient (its d_t may hold anything)
+                    if (on && j0 + j < k && gl == 0) a.dprobs[t * k + j0 + j] = r[j] >= 0 ? x : 0.0f;
+                }
+            }
+            if (a.dy != nullptr) {
+#pragma unroll
+                for (int j = 0; j < kJ; ++j)
+                    if (r[j] >= 0)
+#pragma unroll
+                        for (int u = 0; u < kLaneChunks; ++u) {
+                            const int c = gl + u * L;
+                            if (c < chunks)
+                                __stcs(a.dy + (size_t)r[j] * chunks + c,
+                                       make_float4(p[j] * d[u].x, p[j] * d[u].y, p[j] * d[u].z, p[j] * d[u].w));
+                        }
+            }
+        }
+    }
+}
+
+template <int L>
+cudaError_t launch_short(const CombineGradArgs& a, bool bf16, cudaStream_t s) {
+    const long long items = (long long)a.max_live * ((a.k + kJ - 1) / kJ);
+    const long long want = (items + kCgThreads / L - 1) / (kCgThreads / L), cap = (long long)num_sms() * 10;
+    return launch_dependent(bf16 ? combine_backward_short_kernel<true, L> : combine_backward_short_kernel<false, L>,
+                            dim3((unsigned)(want < cap ? want : cap)), dim3(kCgThreads), 0, s, a);
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -174,10 +267,17 @@ extern "C" moe_status moe_combine_backward(const moe_plan* plan, const void* dou
     a.dprobs = dprobs;
     a.dy = reinterpret_cast<float4*>(dy_rows);
     a.fill = num_sms() * 8;
-    const long long most = plan->max_live > a.fill ? plan->max_live : a.fill;
-    const long long grid = plan->max_live * a.k < most ? plan->max_live * a.k : most;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf16 = (plan->d.flags & MOE_FLAG_OUT_BF16) != 0;
+    const int chunks = a.H / 4;
+    if (chunks <= 32 * kLaneChunks) {
+        const cudaError_t e = chunks <= 8 * kLaneChunks    ? launch_short<8>(a, bf16, s)
+                              : chunks <= 16 * kLaneChunks ? launch_short<16>(a, bf16, s)
+                                                           : launch_short<32>(a, bf16, s);
+        return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
+    const long long most = plan->max_live > a.fill ? plan->max_live : a.fill;
+    const long long grid = plan->max_live * a.k < most ? plan->max_live * a.k : most;
     void (*kern)(CombineGradArgs) = a.k > 8 ? (bf16 ? combine_backward_kernel<true, 16> : combine_backward_kernel<false, 16>)
                                             : (bf16 ? combine_backward_kernel<true, 8> : combine_backward_kernel<false, 8>);
     const cudaError_t e = launch_dependent(kern, dim3((unsigned)grid), dim3(kCgThreads), 0, s, a);
