@@ -126,8 +126,8 @@ __device__ __forceinline__ int2 place_of(const Int8Gemm& p, int num_m, int t) {
 template <int kMode>
 __device__ __forceinline__ int4 tile_of(const Int8Gemm& p, int mt, int rows) {
     if (kMode != kDense) return __ldg(p.tiles + mt);
-    const int m0 = mt * kRouteTile;
-    return make_int4(0, m0, min(kRouteTile, rows - m0), m0);
+    const int m0 = mt * p.tile_rows;
+    return make_int4(0, m0, min(p.tile_rows, rows - m0), m0);
 }
 
 // Each thread of the warp reads 16 consecutive 32-bit columns of its TMEM lane.
@@ -246,8 +246,8 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
     int num_m, rows = 0, widest;
     if (kMode == kDense) {
         rows = p.live != nullptr ? clamp_live(p.live, p.rows) : p.rows;
-        num_m = (rows + kRouteTile - 1) / kRouteTile;
-        widest = min(rows, kRouteTile);
+        num_m = (rows + p.tile_rows - 1) / p.tile_rows;
+        widest = min(rows, p.tile_rows);
     } else {
         num_m = forward_poisoned(p.status_words) ? 0 : (int)p.status_words[kStNumMTiles];
         widest = (int)p.status_words[kStMaxTileRows];

@@ -176,6 +176,24 @@ moe_status check_product(long long rows, int cols_in, const void* w, const float
     return MOE_OK;
 }
 
+// Activation rows of a tile of the wide product: fewer than 256 where the last round of tiles would
+// leave most CTA pairs idle and more, smaller tiles fill it.  A tile takes what its SMs take in, 128
+// weight rows and half of its own each (1236 x 2224 -> 7678: 150 tiles of 256 on 74 pairs, 31.0 us, or
+// 210 of 192, 28.6).
+int dense_tile_rows(long long rows, int n_tiles) {
+    int best = kRouteTile;
+    double least = 0.0;
+    for (int h = kRouteTile; h >= 128 && rows > kRouteTile; h -= 32) {
+        const long long tiles = (rows + h - 1) / h * n_tiles, pairs = num_sms() / 2;
+        const double cost = (double)((tiles + pairs - 1) / pairs) * (128 + h / 2);
+        if (h == kRouteTile || cost < 0.97 * least) {
+            best = h;
+            least = cost;
+        }
+    }
+    return best;
+}
+
 Int8Gemm dense_params(long long rows, int cols_in, const float* x_scales, const float* w_scales, int cols_out,
                       void* out, long long ld_out, int out_bf16, const int* live, unsigned* status) {
     Int8Gemm g{};
@@ -191,6 +209,7 @@ Int8Gemm dense_params(long long rows, int cols_in, const float* x_scales, const 
     g.live = live;
     g.rows = (int)rows;
     g.out_bf16 = out_bf16;
+    g.tile_rows = dense_tile_rows(rows, g.n_tiles);
     // Weights that take much of L2: blocks of eight row tiles, so that the pairs of a wave read few
     // rows of both operands (8192^3: 17 of each operand's 32 tiles a wave instead of 34, 423 -> 398 us
     // sustained); smaller ones stay in L2 in any order, and row by row writes out in longer runs
@@ -216,8 +235,8 @@ bool few_is_faster(const Int8Gemm& g, int cols_in) {
     const double sms = num_sms(), K = cols_in;
     const long long rows = g.rows;
     if (rows > 128ll * 65535) return false;  // row tiles are a grid's second dimension
-    const double wide_n = rows < kRouteTile ? (double)((rows + 31) / 32 * 32) : (double)kRouteTile;
-    const long long wide = (rows + kRouteTile - 1) / kRouteTile * g.n_tiles;
+    const double wide_n = rows < g.tile_rows ? (double)((rows + 31) / 32 * 32) : (double)g.tile_rows;
+    const long long wide = (rows + g.tile_rows - 1) / g.tile_rows * g.n_tiles;
     const double waves = (double)((wide + (long long)(sms / 2) - 1) / (long long)(sms / 2));
     const double t_wide = 3.0 + (rows > 128 ? 2.2 : 0.0) + waves * K * (128.0 + wide_n / 2) / 88e3;
     const double few_n = rows < 128 ? (double)((rows + 15) / 16 * 16) : 128.0;
@@ -233,12 +252,12 @@ moe_status run_dense(const Int8Gemm& g, const int8_t* x, int cols_in, long long 
     CUtensorMap tA;
     BoxMaps8 tB;
     if (!row_map(&tA, w, g.out_cols, cols_in, cols_in, 128)) return MOE_ERR_CUDA;
-    const long long tiles = ((long long)g.rows + kRouteTile - 1) / kRouteTile * g.n_tiles;
+    const long long tiles = ((long long)g.rows + g.tile_rows - 1) / g.tile_rows * g.n_tiles;
     const bool few = few_is_faster(g, cols_in);
     // the heights that tiles of these rows can have: any with a live count, else a full and a last one
     for (int i = 0; i < 8; ++i) {
         const int h = few ? 16 * (i + 1) : 32 * (i + 1);
-        const int top = few ? 128 : kRouteTile, last = (int)(g.rows % top), step = few ? 16 : 32;
+        const int top = few ? 128 : g.tile_rows, last = (int)(g.rows % top), step = few ? 16 : 32;
         const bool used = g.live != nullptr || (g.rows >= top && h == top) ||
                           (last != 0 && h == (last + step - 1) / step * step);
         if (used && !row_map(&tB.m[i], x, g.rows, cols_in, ld_x, 16u * (unsigned)(i + 1))) return MOE_ERR_CUDA;

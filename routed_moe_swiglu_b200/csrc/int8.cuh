@@ -175,7 +175,8 @@ struct Int8Gemm {
     const int* live;                // null: all rows
     int rows;
     int out_bf16;
-    int raster;                     // row tiles of a block of tiles (dense)
+    int tile_rows;                  // activation rows of a tile, a multiple of 32 up to 256
+    int raster;                     // row tiles of a block of tiles
     int early;                      // launched by a kernel that waited before it released this one
 };
 
