@@ -119,7 +119,8 @@ def test_quantize_live_rows(live):
 
 SHAPES = [(1, 16, 1), (1, 64, 3), (2, 128, 17), (7, 144, 96), (31, 272, 64), (33, 256, 257), (64, 2048, 300),
           (100, 96, 1000), (129, 400, 129), (256, 512, 256), (257, 528, 600), (300, 4096, 512), (600, 1024, 1025),
-          (1, 2048, 4096), (16, 8192, 640), (40, 1040, 2000), (5, 16384, 130)]
+          (1, 2048, 4096), (16, 8192, 640), (40, 1040, 2000), (5, 16384, 130), (777, 1040, 3712), (600, 2064, 4096),
+          (1236, 528, 7678), (1922, 80, 1730)]
 
 
 @pytest.mark.parametrize("rows,K,N", SHAPES)
@@ -150,7 +151,7 @@ def test_largest_sums():
 
 
 @pytest.mark.parametrize("bf16", [False, True])
-@pytest.mark.parametrize("rows,live", [(70, 0), (70, 1), (70, 33), (70, 70), (70, 500), (70, -1), (600, 299)])
+@pytest.mark.parametrize("rows,live", [(70, 0), (70, 1), (70, 33), (70, 70), (70, 500), (70, -1), (600, 299), (1500, 1111)])
 def test_live_rows_strides_and_odd_addresses(rows, live, bf16):
     """Rows past the live count and columns past N keep their bytes; x rows of a longer stride, out
     rows of an odd stride at an odd address."""
