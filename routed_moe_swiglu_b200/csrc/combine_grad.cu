@@ -2,13 +2,14 @@
 //
 // The combine is out_t = sum_j p[t,j] y[r(t,j)], so with d_t the gradient of
 // out_t:  dprobs[t,j] = <d_t, y[r(t,j)]>  and  dy[r(t,j)] = p[t,j] d_t.
-// Both are one pass over the y rows: a block holds a slice of d_t in registers
-// and walks the token's rows, so that d_t is read once for all of them.  The
-// dot products are sums of 128 threads' partial sums in fp32, added in a fixed
-// order whatever the number of routes a block takes.
+// Both are one pass over the y rows with d_t in registers, so that d_t is read
+// once for all of a token's rows: rows of up to 2,048 elements a token a group of
+// lanes, longer ones a token a block (with few tokens the routes are spread, each
+// item reading d_t again from L2).  A dot product is a sum of lanes' or threads'
+// partial sums in fp32, added in an order fixed by H alone.
 //
 // Bound by memory: y is read and dy written once.  8,192 tokens x 8 routes x
-// 2,048: 186 us for 1.14 GB, 6.1 TB/s, 0.94 of the measured copy rate; 333 x 6 x
+// 2,048: 181 us for 1.14 GB, 6.3 TB/s, 0.96 of the measured copy rate; 333 x 6 x
 // 2,688 with bf16 gradients: 10.7 us for 45 MB, where start and end count.
 #include "moe_internal.cuh"
 
@@ -17,8 +18,7 @@ namespace {
 
 constexpr int kCgThreads = 128;
 constexpr int kCgWarps = kCgThreads / 32;
-constexpr int kLaneChunks = 4;  // of a short row, a lane's 16-byte chunks at most
-constexpr int kJ = 4;           // of a short row's token, routes at a time
+constexpr int kRowChunks = 512;  // 16-byte chunks of a row that a warp takes
 
 struct CombineGradArgs {
     const void* dout;
@@ -90,7 +90,7 @@ __device__ __forceinline__ void walk(const CombineGradArgs& a, int t, int c, int
 // Items are (token, group of its routes).  With fewer live tokens than `fill` the k routes are spread
 // over several blocks, each reading d_t again (from L2) for its own rows.  With more, a block for
 // each token leaves the SMs no uneven last round (8,192 tokens x 8 x 2,048: 186 us, against 200 with
-// eight blocks an SM that walk the tokens).
+// eight blocks an SM that walk the tokens; the lane groups below take rows of that length now).
 // kMost: the most routes a token may have, 8 or 16.
 template <bool kBf16, int kMost>
 __global__ void __launch_bounds__(kCgThreads, kMost > 8 ? 5 : 7) combine_backward_kernel(const CombineGradArgs a) {
@@ -149,28 +149,29 @@ __global__ void __launch_bounds__(kCgThreads, kMost > 8 ? 5 : 7) combine_backwar
     }
 }
 
-// Short rows (H <= 4 * kLaneChunks * 32): L lanes hold d_t, at most kLaneChunks 16-byte chunks each, and
-// walk the token's rows four at a time; 32 / L tokens a warp.  A block a token would leave most of its
-// threads without a chunk (46,692 tokens x 1 x 80: 10.2 us, 87 with a block a token).
-template <bool kBf16, int L>
-__global__ void __launch_bounds__(kCgThreads, 5) combine_backward_short_kernel(const CombineGradArgs a) {
+// Rows that L lanes can hold: d_t in registers, C 16-byte chunks a lane, and the token's rows J at a time;
+// 32 / L tokens a warp.  A block a token has a chain of launch, loads and meetings for each, and leaves
+// threads without a chunk (46,692 tokens x 1 x 80: 10.2 us, 87 with a block a token; 36,057 x 2 x 520:
+// 72 and 117; 8,192 x 8 x 2,048: 181 and 186; past 2,048 the registers of d_t leave too few warps).
+template <bool kBf16, int L, int C, int J, int kBlocks>
+__global__ void __launch_bounds__(kCgThreads, kBlocks) combine_backward_rows_kernel(const CombineGradArgs a) {
     pdl_trigger();
     pdl_wait();
     const int n = clamp_live(a.live, a.max_live), k = a.k, chunks = a.H / 4;
     const int gl = threadIdx.x & (L - 1);
     const long long step = (long long)gridDim.x * (kCgThreads / L);
-    // items: a token, or with few of them kJ of its routes
-    const int batches = (k + kJ - 1) / kJ;
+    // items: a token, or with few of them J of its routes
+    const int batches = (k + J - 1) / J;
     const int split = (long long)n * batches <= step ? batches : 1;
     // every lane of a warp goes round as often as its first group
     for (long long i0 = (long long)blockIdx.x * (kCgThreads / L) + (threadIdx.x & ~31) / L; i0 < (long long)n * split;
          i0 += step) {
         const long long item = i0 + (threadIdx.x & 31) / L, t = item / split;
         const bool on = t < n;
-        const int j_lo = (int)(item - t * split) * kJ;
-        float4 d[kLaneChunks];
+        const int j_lo = (int)(item - t * split) * J;
+        float4 d[C];
 #pragma unroll
-        for (int u = 0; u < kLaneChunks; ++u) {
+        for (int u = 0; u < C; ++u) {
             const int c = gl + u * L;
             d[u] = on && c < chunks ? load_grad<kBf16>(a.dout, (size_t)t * chunks + c) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
@@ -183,12 +184,12 @@ __global__ void __launch_bounds__(kCgThreads, 5) combine_backward_short_kernel(c
                 row[i] = __ldg(a.rows + t * k + gl + i * L);
                 pr[i] = __ldg(a.probs + t * k + gl + i * L);
             }
-        for (int j0 = j_lo, i = 0; i < (split > 1 ? 1 : batches); ++i, j0 += kJ) {
-            int r[kJ];
-            float p[kJ];
-            float4 v[kJ][kLaneChunks];
+        for (int j0 = j_lo, i = 0; i < (split > 1 ? 1 : batches); ++i, j0 += J) {
+            int r[J];
+            float p[J];
+            float4 v[J][C];
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) {
+            for (int j = 0; j < J; ++j) {
                 const int at = j0 + j;
                 const bool second = at >= L;
                 r[j] = __shfl_sync(0xffffffffu, second ? row[1] : row[0], at & (L - 1), L);
@@ -197,31 +198,32 @@ __global__ void __launch_bounds__(kCgThreads, 5) combine_backward_short_kernel(c
             }
             if (a.dprobs != nullptr) {
 #pragma unroll
-                for (int j = 0; j < kJ; ++j)
+                for (int j = 0; j < J; ++j)
 #pragma unroll
-                    for (int u = 0; u < kLaneChunks; ++u) {
+                    for (int u = 0; u < C; ++u) {
                         const int c = gl + u * L;
                         v[j][u] = r[j] >= 0 && c < chunks ? __ldg(a.y + (size_t)r[j] * chunks + c)
                                                           : make_float4(0.f, 0.f, 0.f, 0.f);
                     }
+                float mine = 0.0f;
 #pragma unroll
-                for (int j = 0; j < kJ; ++j) {
+                for (int j = 0; j < J; ++j) {
                     float x = 0.0f;
 #pragma unroll
-                    for (int u = 0; u < kLaneChunks; ++u)
+                    for (int u = 0; u < C; ++u)
                         x = fmaf(d[u].w, v[j][u].w, fmaf(d[u].z, v[j][u].z, fmaf(d[u].y, v[j][u].y, fmaf(d[u].x, v[j][u].x, x))));
 #pragma unroll
                     for (int o = L / 2; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-                    // a route without a row has no gradient (its d_t may hold anything)
-                    if (on && j0 + j < k && gl == 0) a.dprobs[t * k + j0 + j] = r[j] >= 0 ? x : 0.0f;
+                    if (gl == j) mine = r[j] >= 0 ? x : 0.0f;  // a route without a row has no gradient
                 }
+                if (on && gl < J && j0 + gl < k) a.dprobs[t * k + j0 + gl] = mine;
             }
             if (a.dy != nullptr) {
 #pragma unroll
-                for (int j = 0; j < kJ; ++j)
+                for (int j = 0; j < J; ++j)
                     if (r[j] >= 0)
 #pragma unroll
-                        for (int u = 0; u < kLaneChunks; ++u) {
+                        for (int u = 0; u < C; ++u) {
                             const int c = gl + u * L;
                             if (c < chunks)
                                 __stcs(a.dy + (size_t)r[j] * chunks + c,
@@ -232,11 +234,12 @@ __global__ void __launch_bounds__(kCgThreads, 5) combine_backward_short_kernel(c
     }
 }
 
-template <int L>
-cudaError_t launch_short(const CombineGradArgs& a, bool bf16, cudaStream_t s) {
-    const long long items = (long long)a.max_live * ((a.k + kJ - 1) / kJ);
-    const long long want = (items + kCgThreads / L - 1) / (kCgThreads / L), cap = (long long)num_sms() * 10;
-    return launch_dependent(bf16 ? combine_backward_short_kernel<true, L> : combine_backward_short_kernel<false, L>,
+template <int L, int C, int J, int kBlocks>
+cudaError_t launch_rows(const CombineGradArgs& a, bool bf16, cudaStream_t s) {
+    const long long items = (long long)a.max_live * ((a.k + J - 1) / J);
+    const long long want = (items + kCgThreads / L - 1) / (kCgThreads / L), cap = (long long)num_sms() * kBlocks * 2;
+    return launch_dependent(bf16 ? combine_backward_rows_kernel<true, L, C, J, kBlocks>
+                                 : combine_backward_rows_kernel<false, L, C, J, kBlocks>,
                             dim3((unsigned)(want < cap ? want : cap)), dim3(kCgThreads), 0, s, a);
 }
 
@@ -270,10 +273,12 @@ extern "C" moe_status moe_combine_backward(const moe_plan* plan, const void* dou
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf16 = (plan->d.flags & MOE_FLAG_OUT_BF16) != 0;
     const int chunks = a.H / 4;
-    if (chunks <= 32 * kLaneChunks) {
-        const cudaError_t e = chunks <= 8 * kLaneChunks    ? launch_short<8>(a, bf16, s)
-                              : chunks <= 16 * kLaneChunks ? launch_short<16>(a, bf16, s)
-                                                           : launch_short<32>(a, bf16, s);
+    if (chunks <= kRowChunks) {
+        const cudaError_t e = chunks <= 32    ? launch_rows<8, 4, 4, 5>(a, bf16, s)
+                              : chunks <= 64  ? launch_rows<16, 4, 4, 5>(a, bf16, s)
+                              : chunks <= 128 ? launch_rows<32, 4, 4, 5>(a, bf16, s)
+                              : chunks <= 256 ? launch_rows<32, 8, 2, 4>(a, bf16, s)
+                                              : launch_rows<32, 16, 1, 3>(a, bf16, s);
         return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     }
     const long long most = plan->max_live > a.fill ? plan->max_live : a.fill;

@@ -393,7 +393,7 @@ def test_many_tokens():
 @pytest.mark.parametrize("T,H,k,out,cap", [
     (1, 8, 1, "fp32", 1), (1, 2048, 16, "bf16", 3), (7, 136, 3, "fp32", 7), (300, 2688, 6, "bf16", 310),
     (33, 4096, 9, "fp32", 40), (5000, 64, 8, "bf16", 5000), (0, 64, 2, "fp32", 4), (70, 512, 16, "bf16", 75),
-    (9, 128, 16, "fp32", 9), (45, 248, 13, "fp32", 45), (33, 520, 5, "bf16", 33), (20011, 80, 1, "fp32", 20011)])
+    (9, 128, 16, "fp32", 9), (45, 248, 13, "fp32", 45), (33, 520, 5, "bf16", 33), (50, 1032, 7, "fp32", 61), (3001, 1984, 2, "bf16", 3001), (3, 2056, 16, "fp32", 5), (20011, 80, 1, "fp32", 20011)])
 def test_combine_backward(T, H, k, out, cap):
     g = torch.Generator().manual_seed(T + H)
     plan = rm.moe_plan_create(hidden=H, ffn=64, num_experts=16, top_k=k, capacity=cap, out_dtype=out)
