@@ -20,6 +20,7 @@
 // One token, 2048 -> 4096: 5.95 us, where reading the weights takes 1.3: launch,
 // cluster start, quantising, one chain of loads, the exchange of partial sums and
 // the end, about a microsecond each.  As two launches of the wide kernels 8.8 us.
+// Sixteen tokens: 7.3 us, their rows' loads side by side (9.0 row after row).
 #include "int8.cuh"
 #include "ptx.cuh"
 
@@ -225,19 +226,34 @@ __global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid
         }
         cluster_sync();
         if (wt >= 0) {
-            for (int i = 0; i < kRows; ++i) {
-                const int r = warp - 2 + 4 * i;
-                if (r >= nt) break;
-                uint32_t m = 0u;
+            // lane l works out row l % kRows of the warp's; all rows are then read side by side
+            const int mine = warp - 2 + 4 * (lane % kRows);
+            uint32_t m = 0u;
 #pragma unroll
-                for (int c = 0; c < kMaxCluster; ++c) m = c < S ? max(m, sh.amax[c][r]) : m;
-                const Int8Row row = int8_row(__uint_as_float(m));
-                const uint4* x = a.x + (size_t)(m0 + r) * a.ld_x + (size_t)k0 * 16;
-                uint8_t* dst = sB + r * 128;
-                for (int u = lane; u < units; u += 32) {
-                    const uint2 lo = int8_codes8(__ldg(x + 2 * u), row), hi = int8_codes8(__ldg(x + 2 * u + 1), row);
+            for (int c = 0; c < kMaxCluster; ++c) m = c < S && mine < nt ? max(m, sh.amax[c][mine]) : m;
+            const Int8Row own = int8_row(__uint_as_float(m));
+            Int8Row row[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                row[i].scale = __shfl_sync(0xffffffffu, own.scale, i);
+                row[i].inv = __shfl_sync(0xffffffffu, own.inv, i);
+                row[i].divide = __shfl_sync(0xffffffffu, (int)own.divide, i) != 0;
+            }
+            for (int u = lane; u < units; u += 32) {
+                uint4 v[kRows][2];
+#pragma unroll
+                for (int i = 0; i < kRows; ++i)
+                    if (warp - 2 + 4 * i < nt) {
+                        v[i][0] = __ldg(src[i] + 2 * u);
+                        v[i][1] = __ldg(src[i] + 2 * u + 1);
+                    }
+#pragma unroll
+                for (int i = 0; i < kRows; ++i) {
+                    const int r = warp - 2 + 4 * i;
+                    if (r >= nt) break;
+                    const uint2 lo = int8_codes8(v[i][0], row[i]), hi = int8_codes8(v[i][1], row[i]);
                     // the 128-byte swizzle: 16-byte chunk c of row r lies at c ^ (r % 8)
-                    *reinterpret_cast<uint4*>(dst + (u >> 3) * C::kBSlot + (((u & 7) ^ (r & 7)) << 4)) =
+                    *reinterpret_cast<uint4*>(sB + r * 128 + (u >> 3) * C::kBSlot + (((u & 7) ^ (r & 7)) << 4)) =
                         make_uint4(lo.x, lo.y, hi.x, hi.y);
                 }
             }
