@@ -521,7 +521,7 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
                                                           (size_t)(ti.y + c * kChunk) * (size_t)p.out_ld + f0
                                                     : nullptr;
                 if (glu) {
-                    // silu(g) * u = g * u / (1 + exp(-g))
+                    // silu(g) * u, silu first: g * u alone may pass fp32's range
                     const int r0 = lane < 16 ? 0 : kHalf;
                     const float4* xs4 = reinterpret_cast<const float4*>(s_xs + i * kChunk + r0);
                     float hv[kHalf];
@@ -535,7 +535,7 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
                             gt = make_float2(clamp_nan(gt.x, p.clamp), clamp_nan(gt.y, p.clamp));
                             up = make_float2(clamp_nan(up.x, p.clamp), clamp_nan(up.y, p.clamp));
                         }
-                        float2 o = mul2(mul2(gt, up), sigmoid_approx2(gt));
+                        float2 o = mul2(mul2(gt, sigmoid_approx2(gt)), up);
                         if (p.route_probs != nullptr)
                             o = mul2(o, make_float2(__shfl_sync(0xffffffffu, pv, r0 + 2 * q),
                                                     __shfl_sync(0xffffffffu, pv, r0 + 2 * q + 1)));

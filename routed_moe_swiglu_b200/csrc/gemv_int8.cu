@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kGvThreads) moe_gemv_int8_kernel(const GemvArg
         const float u = p.clamp > 0.0f ? clamp_nan(vb, p.clamp) : vb;
         const float pr = p.route_probs != nullptr ? __ldg(p.route_probs + __ldg(p.perm + ti.w + t)) : 1.0f;
         if (swiglu) {
-            float hv = g * u * sigmoid_approx(g);
+            float hv = g * sigmoid_approx(g) * u;
             if (p.route_probs != nullptr) hv *= pr;
             h[0] = __float2bfloat16_rn(hv);
         } else {

@@ -145,7 +145,8 @@ __device__ __forceinline__ float clamp_nan(float x, float c) {
     return r;
 }
 // 1 / (1 + exp(-g)) from the approximate exponential and reciprocal (2^-22 and 1 ulp; the
-// exponent's rounding adds |g| 2^-24): far below the bf16 step that h is rounded to.
+// exponent's rounding adds |g| 2^-24): far below the bf16 step that h is rounded to.  0 below -87.3,
+// where it is a subnormal; the other precisions' quotient is 0 there too.
 __device__ __forceinline__ float sigmoid_approx(float g) {
     float e, r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));

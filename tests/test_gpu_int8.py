@@ -501,6 +501,44 @@ def test_a_token_of_nan_stays_alone():
         assert torch.isnan(bad[[7, 9]]).all() and torch.equal(bad[keep], good[keep])
 
 
+@pytest.mark.parametrize("T", [3, 200])
+@pytest.mark.parametrize("in_fc1", [False, True])
+@pytest.mark.parametrize("huge", [False, True])
+def test_gate_times_up_beyond_fp32(T, in_fc1, huge):
+    """Finite pre-activations whose product passes fp32's range, the gate far below zero: h is
+    silu(gate) * up and stays finite, on plans of few rows and of many."""
+    H, F, E = 128, 24, 2
+    pairs = [[-80.0, 1e37], [-40.0, 2e38], [-2e19, 2e19], [-60.0, -1e37], [-3e20, -3e20], [0.5, 3.0]]
+    if huge:
+        pairs += [[2.0, 1e37], [-1.0, 3e38]]
+    pairs = torch.tensor(pairs, dtype=torch.float64).repeat(F // len(pairs), 1)
+    even = torch.ones(E, F, H, dtype=torch.float64)
+    wg, wu = ((even * pairs[:, i].view(1, F, 1) / H).to(torch.bfloat16) for i in (0, 1))
+    wd = (torch.randn((E, H, F), generator=torch.Generator().manual_seed(8)) * 1e-20).to(torch.bfloat16)
+    x = torch.tensor([1.0, 0.5, 0.9375])[torch.arange(T) % 3].view(T, 1).expand(T, H).to(torch.bfloat16).contiguous()
+    ids, probs = (torch.arange(T) % E).int().view(T, 1), torch.full((T, 1), 0.75)
+    m = GpuMoe(H, F, E, 1, T, (wg, wu, wd), precision="int8", probs_in_fc1=in_fc1)
+    out = m.forward(x.cuda(), T, ids=ids.cuda(), probs=probs.cuda())
+    assert m.status() == 0
+    v = m.views()
+    rows = torch.from_numpy(m.read_i32(v["inv"], T)).long().cuda()
+    h = _ws(m, v["h_bf16"], v["rows_padded"] * _pad128(F), torch.bfloat16).view(-1, _pad128(F))[rows].cpu()[:, :F]
+    (xq, xs), codes = quantize_ref(x), [quantize_ref(w) for w in (wg, wu)]
+    g, u = (torch.stack([(xq[t].double() @ wq[t % E].double().T) * xs[t].double() * ws[t % E].double() for t in range(T)])
+            for wq, ws in codes)
+    assert torch.isfinite(g.float()).all() and torch.isfinite(u.float()).all() and ((g.float() * u.float()).isinf()).any()
+    # three roundings of g and the exponent's own move silu(g) by 4 |g| u; u's, the exponential's, the
+    # quotient's and the products' by 16 u more; then the bf16 rounding.  Below -87 the sigmoid is 0.
+    ref = g / (1 + torch.exp(-g)) * u * (0.75 if in_fc1 else 1.0)
+    assert ((h.double() - ref).abs() <= (2.0 ** -8 + (4 * g.abs().clamp(max=100) + 16) * U) * ref.abs()).all()
+    # down: of huge rows the sum times the row's scale, up to 8e37 * 127, passes fp32's range before
+    # the channel's scale is applied, as the order of the two products has it
+    y = _ws(m, v["y"], v["rows_padded"] * H, torch.float32).view(-1, H)[rows].cpu()
+    (hq, hs), (dq, ds) = quantize_ref(h), quantize_ref(wd)
+    _same(y, torch.cat([product_ref(hq[t:t + 1], hs[t:t + 1], dq[t % E], ds[t % E], False) for t in range(T)]))
+    assert not torch.isnan(out).any() and (huge or torch.isfinite(out).all())
+
+
 def test_batch_invariance_graph_and_noalloc():
     H, F, E, k = 512, 512, 16, 4
     x, logits, weights = workloads.small_case(H, F, E, k, 600, seed=42)
