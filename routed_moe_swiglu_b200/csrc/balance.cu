@@ -808,8 +808,10 @@ __global__ void __launch_bounds__(kGradThreads, kGradBlocks<V>) route_backward_k
             sum = group_sum<L>(sum);
             dot = group_sum<L>(dot);
             // p (as (c - <c, p>) + zs lse), with p = x / sum; 0 where the token does not count
+            // (both factors: `as` and zs hold the caller's scale, which may have overflowed)
             const float inv = counted ? __frcp_rn(sum) : 0.0f;
-            const float slope = as * inv, base = counted ? fmaf(zs, lse, -as * (dot * inv)) * inv : 0.0f;
+            const float slope = counted ? as * inv : 0.0f;
+            const float base = counted ? fmaf(zs, lse, -as * (dot * inv)) * inv : 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v) x[v] *= fmaf(slope, cnt[v], base);
         } else {

@@ -495,3 +495,22 @@ def test_a_training_step_of_the_router(precision):
     r.backward(losses=False)
     mine = r.dlogits[:T].double().gather(1, ids[:T].long()) * u
     assert abs(float(mine.sum()) - num) <= 2e-5 * float(mine.abs().sum()) + 1e-6 * float((rows.abs() * dout[:T, None].abs()).sum(2).max())
+
+
+@pytest.mark.parametrize("grads", [(float("inf"), 1.0), (float("nan"), float("nan")), (-float("inf"), float("inf")), (3e38, 0.0)])
+def test_rows_that_do_not_count_stay_zero_when_the_gradient_scale_overflowed(grads):
+    """Masked tokens, tokens outside every sequence and rows of -infinity get zeros whatever the losses'
+    gradients are, before and behind counted rows that are lost to them."""
+    T, E, k = 60000, 60, 4  # several rows after one another in every group of lanes
+    q = _problem(T, E, k, 3, seed=31, masked=True, cap=T + 10, offsets=[5, 20000, 20000, 59000])
+    q["logits"][40000:40100] = float("-inf")
+    alive = q["mask"][:T] != 0
+    alive[:5] = alive[59000:] = alive[40000:40100] = False
+    r = _Run(q)
+    r.forward(1e10, 0.1)
+    for chosen in (False, True):
+        r.dlogits.fill_(-5.0)
+        r.backward(torch.tensor(grads, device="cuda"), chosen=chosen)
+        d = r.dlogits.cpu()
+        assert not torch.isfinite(d[:T][alive]).all(dim=1).any()
+        assert (d[:T][~alive] == 0).all() and (d[T:] == -5.0).all()
