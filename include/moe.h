@@ -279,6 +279,8 @@ moe_status moe_route_topk(const moe_plan* plan, const float* logits, const int* 
  * read; seq_offsets int32 [num_seqs + 1], nondecreasing: sequence s is the live
  * rows [seq_offsets[s], seq_offsets[s+1]) (bounds past the live count are clamped
  * to it; sequences may be empty), or NULL with num_seqs 1 for all live rows.
+ * Offsets that decrease (once clamped) make both losses and all of grad_scales
+ * NaN, and what the other outputs then hold has no meaning.
  * num_seqs: 1 .. MOE_MAX_SEQS.  A NaN or +infinity among a counted token's logits
  * makes the losses and its expert sums NaN.  Sums are held in fp32 and added in a
  * fixed order: the same inputs give the same bits.  workspace:

@@ -38,6 +38,7 @@
 // the chain of launches and meetings: 64 tokens x 8 experts, one cluster and one
 // launch, 6.6 us and the gradient 3.2; 4,099 x 128 in seven sequences 10.6 and 4.5;
 // 3,001 x 1,000 15 and 10.
+#include <climits>
 #include <cmath>
 
 #include "moe_internal.cuh"
@@ -61,6 +62,7 @@ constexpr int kFinBlocks = 8;               // of the finishing kernel where it 
 constexpr int kFinGroup = 8;                // its warps that add an item's slots together
 constexpr int kFinCols = 32;                // columns of an item of the finish
 constexpr int kBatch = 8;                   // loads of the finish in flight
+constexpr int kBadOffsets = 1 << 17;        // added to a count of sequences by each thread that found a decrease
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct BalanceArgs {
@@ -83,7 +85,7 @@ struct BalanceArgs {
     int* slot_n;        // [slots]
     float* seq_dot;     // [num_seqs][col blocks]
     float* seq_z;       // [num_seqs]
-    int* seq_n;         // [num_seqs]
+    int* seq_n;         // [num_seqs]; -1 where the offsets decrease
     unsigned* ticket;   // zeroed by the sums' kernel, counted by the finishing one
 };
 
@@ -386,7 +388,7 @@ __device__ __forceinline__ void balance_stats(const BalanceArgs& a, int n, float
         }
     };
     // this warp's segment, and the row of its run's counts (at least two segments each, but for a run
-    // alone: at most kCutRuns rows)
+    // alone: below kCutRuns, whatever the offsets)
     int seg_lo = 0, seg_hi = 0, row = 0, cut;
     int step = kGroups;
     if (alone) {  // every warp in turn
@@ -489,7 +491,9 @@ __device__ __forceinline__ void balance_stats(const BalanceArgs& a, int n, float
         join(s0, 0, cut, s_cnt);
     else
         sweep([&](int base, const Run&, int m, int first, int runs) {
-            for (unsigned cuts = __ballot_sync(0xffffffffu, m > 0); cuts != 0u; cuts &= cuts - 1, ++runs) {
+            // (more than kCutRuns only where the offsets decrease, which finish_total finds)
+            for (unsigned cuts = __ballot_sync(0xffffffffu, m > 0); cuts != 0u && runs < kCutRuns;
+                 cuts &= cuts - 1, ++runs) {
                 const int from = __ffs(cuts) - 1, w0 = __shfl_sync(0xffffffffu, first, from);
                 join(base + from, w0, w0 + __shfl_sync(0xffffffffu, m, from), s_cnt + runs * E);
             }
@@ -568,7 +572,7 @@ __device__ __forceinline__ void finish_items(const BalanceArgs& a, int n, int ra
                 a.seq_dot[it] = dot;
                 if (cb == 0) {
                     a.seq_z[s] = z;
-                    a.seq_n[s] = m;
+                    a.seq_n[s] = se < sb ? -1 : m;
                 }
             }
         }
@@ -577,8 +581,10 @@ __device__ __forceinline__ void finish_items(const BalanceArgs& a, int n, int ra
 }
 
 // One block: S', T and the z sum, then the sequences' factors and the losses.  Each thread takes
-// every blockDim-th sequence, and the threads' sums are added in a fixed order.
+// every blockDim-th sequence, and the threads' sums are added in a fixed order.  Offsets that
+// decrease have no sums: every factor and loss is then NaN.
 __device__ __forceinline__ void finish_total(const BalanceArgs& a, FinishShared& sh) {
+    static_assert(MOE_MAX_SEQS < kBadOffsets && kFinThreads <= INT_MAX / kBadOffsets - 1, "counted in `filled`");
     const int S = a.num_seqs, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const int used = min(warps, (S + 31) / 32);  // warps that have a sequence
     const int col_blocks = (a.E + kFinCols - 1) / kFinCols;
@@ -600,13 +606,16 @@ __device__ __forceinline__ void finish_total(const BalanceArgs& a, FinishShared&
     const int m0 = mine ? __ldcg(a.seq_n + threadIdx.x) : 0;
     float z = mine ? __ldcg(a.seq_z + threadIdx.x) : 0.0f;
     const float dot0 = mine ? dot_of(threadIdx.x) : 0.0f;
+    bool bad = m0 < 0;
     int filled = m0 > 0, total = m0;
     for (int s = threadIdx.x + blockDim.x; s < S; s += blockDim.x) {
         const int m = __ldcg(a.seq_n + s);
+        bad |= m < 0;
         filled += m > 0;
         total += m;
         z += __ldcg(a.seq_z + s);
     }
+    if (bad) filled += kBadOffsets;
     filled = __reduce_add_sync(0xffffffffu, filled);
     total = __reduce_add_sync(0xffffffffu, total);
     z = group_sum<32>(z);
@@ -626,6 +635,8 @@ __device__ __forceinline__ void finish_total(const BalanceArgs& a, FinishShared&
         }
         __syncthreads();
     }
+    bad = filled >= kBadOffsets;
+    const float nan = __uint_as_float(0x7fc00000u);
     const float scale = a.balance_coef * (float)a.E / ((float)max(filled, 1) * (float)a.k);
     float loss = 0.0f;
     for (int s = threadIdx.x; s < S; s += blockDim.x) {
@@ -633,7 +644,7 @@ __device__ __forceinline__ void finish_total(const BalanceArgs& a, FinishShared&
         const int m = first ? m0 : __ldcg(a.seq_n + s);
         const float as = m > 0 ? scale / (float)m / (float)m : 0.0f;
         if (m > 0) loss = fmaf(as, first ? dot0 : dot_of(s), loss);
-        a.grad_scales[s] = as;
+        a.grad_scales[s] = bad ? nan : as;
     }
     loss = group_sum<32>(loss);
     if (used > 1) {
@@ -644,9 +655,9 @@ __device__ __forceinline__ void finish_total(const BalanceArgs& a, FinishShared&
     }
     if (threadIdx.x == 0) {
         const float zt = total > 0 ? a.z_coef / (float)total : 0.0f;
-        a.losses[0] = loss;
-        a.losses[1] = zt != 0.0f ? zt * z : 0.0f;  // without a z loss, 0 even where lse^2 overflows
-        a.grad_scales[S] = 2.0f * zt;
+        a.losses[0] = bad ? nan : loss;
+        a.losses[1] = bad ? nan : zt != 0.0f ? zt * z : 0.0f;  // without a z loss, 0 even where lse^2 overflows
+        a.grad_scales[S] = bad ? nan : 2.0f * zt;
     }
 }
 

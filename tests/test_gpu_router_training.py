@@ -514,3 +514,31 @@ def test_rows_that_do_not_count_stay_zero_when_the_gradient_scale_overflowed(gra
         d = r.dlogits.cpu()
         assert not torch.isfinite(d[:T][alive]).all(dim=1).any()
         assert (d[:T][~alive] == 0).all() and (d[T:] == -5.0).all()
+
+
+@pytest.mark.parametrize("T,E,k,S", [(40, 16, 2, 3), (2000, 64, 4, 200), (3000, 1024, 4, 300), (70000, 32, 2, 90), (5000, 128, 8, 5000)])
+def test_offsets_that_decrease(T, E, k, S):
+    """Losses and factors are NaN, rows past the live count keep their bytes, and the next call is as ever."""
+    good = _problem(T, E, k, S, seed=T, cap=T + 5)
+    r = _Run(good)
+    r.forward(0.1, 0.1)
+    want = [t.clone() for t in (r.losses, r.scales, r.counts, r.sums)]
+    assert torch.isfinite(r.losses).all()
+    off, g = r.dev["off"], torch.Generator().manual_seed(S)
+    tables = [torch.where(torch.arange(S + 1) % 2 == 0, 0, T), torch.randint(-9, T + 9, (S + 1,), generator=g),
+              torch.arange(S, -1, -1), torch.cat([off[:-1].cpu(), off[-2:-1].cpu() - 1])]
+    if S > 3:  # one decrease in the middle
+        tables.append(off.cpu().clone())
+        tables[-1][S // 2] = -1 if int(off[S // 2 - 1]) else T
+    for table in tables:
+        clamped = table.clamp(0, T)
+        assert bool((clamped[1:] < clamped[:-1]).any())
+        off.copy_(table.int())
+        r.forward(0.1, 0.1)
+        assert torch.isnan(r.losses).all() and torch.isnan(r.scales).all() and (r.lse[T:] == -5.0).all()
+        r.backward()
+        assert (r.dlogits[T:] == -5.0).all()
+    off.copy_(good["off"])
+    r.forward(0.1, 0.1)
+    for a, b in zip((r.losses, r.scales, r.counts, r.sums), want):
+        assert torch.equal(a, b)
