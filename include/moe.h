@@ -594,8 +594,16 @@ typedef struct {
     const void* h_bf16;     /* int8 only: the bf16 SwiGLU rows [rows_padded,
                                ceil(F/128)*128] before they are quantised          */
 } moe_workspace_views;
+/* views_bytes: sizeof of the caller's struct, a multiple of 8 from that of the
+ * struct's first fifteen fields on; fields past those this library knows are
+ * zeroed.  moe_get_workspace_views, which programs built when the struct ended
+ * with h_fp32 call, writes those fifteen; in C and C++ its name takes the sized
+ * call with the struct above. */
+moe_status moe_get_workspace_views_sized(const moe_plan* plan, const void* workspace, void* views,
+                                         size_t views_bytes);
 moe_status moe_get_workspace_views(const moe_plan* plan, const void* workspace,
                                    moe_workspace_views* views);
+#define moe_get_workspace_views(plan, ws, views) moe_get_workspace_views_sized((plan), (ws), (views), sizeof(*(views)))
 
 /* Copy the workspace's device status word to *flags_host.  Synchronises
  * `stream` (the only call that does). */
@@ -622,7 +630,7 @@ moe_status moe_check_bounded_wait(unsigned long long limit_ns, unsigned* status_
 /* Static string for a status code. */
 const char* moe_status_string(moe_status s);
 
-/* Library version, e.g. "0.1.0". */
+/* Library version, e.g. "0.2.0". */
 const char* moe_version(void);
 
 #ifdef __cplusplus

@@ -122,7 +122,7 @@ def load_library():
         "moe_ep_ipc_handle": ([P, P], I),
         "moe_ep_ipc_open": ([P, ctypes.POINTER(P)], I),
         "moe_ep_ipc_close": ([P], I),
-        "moe_get_workspace_views": ([P, P, ctypes.POINTER(_Views)], I),
+        "moe_get_workspace_views_sized": ([P, P, ctypes.POINTER(_Views), SZ], I),
         "moe_get_device_status": ([P, ctypes.POINTER(ctypes.c_uint), P], I),
         "moe_clear_device_status": ([P, P], I),
         "moe_check_bounded_wait": ([ctypes.c_ulonglong, P, P, P], I),
@@ -695,7 +695,7 @@ def moe_forward_with_events(plan: Plan, x, kernel_buf, live_count, out, workspac
 
 def moe_get_workspace_views(plan: Plan, workspace) -> dict:
     v = _Views()
-    _check(load_library().moe_get_workspace_views(plan.handle, _ptr(workspace), ctypes.byref(v)),
+    _check(load_library().moe_get_workspace_views_sized(plan.handle, _ptr(workspace), ctypes.byref(v), ctypes.sizeof(v)),
            "moe_get_workspace_views")
     d = {n: getattr(v, n) for n, _ in _Views._fields_}
     d["base"] = workspace.data_ptr()

@@ -2,6 +2,7 @@
 // layouts, TMA descriptors and the launch sequence of the forward.
 #include <cudaTypedefs.h>
 
+#include <cstddef>
 #include <cstdlib>
 #include <cstring>
 #include <new>
@@ -160,7 +161,7 @@ using namespace moe;
 
 extern "C" {
 
-const char* moe_version(void) { return "0.1.0"; }
+const char* moe_version(void) { return "0.2.0"; }
 
 const char* moe_status_string(moe_status s) {
     switch (s) {
@@ -786,11 +787,15 @@ moe_status moe_ep_ipc_close(void* dev_ptr) {
     return cudaIpcCloseMemHandle(dev_ptr) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
-moe_status moe_get_workspace_views(const moe_plan* plan, const void* workspace, moe_workspace_views* v) {
-    if (plan == nullptr || workspace == nullptr || v == nullptr) return MOE_ERR_INVALID_ARG;
+// The struct as it was first: up to and with h_fp32.
+static constexpr size_t kFirstViewsBytes = offsetof(moe_workspace_views, y);
+
+moe_status moe_get_workspace_views_sized(const moe_plan* plan, const void* workspace, void* views, size_t views_bytes) {
+    if (plan == nullptr || workspace == nullptr || views == nullptr) return MOE_ERR_INVALID_ARG;
+    if (views_bytes < kFirstViewsBytes || views_bytes % sizeof(void*) != 0) return MOE_ERR_INVALID_ARG;
     const uint8_t* ws = static_cast<const uint8_t*>(workspace);
     const WsLayout& L = plan->ws;
-    std::memset(v, 0, sizeof(*v));
+    moe_workspace_views known{}, *v = &known;
     v->route_ids = reinterpret_cast<const int*>(ws + L.r_ids);
     v->route_probs = reinterpret_cast<const float*>(ws + L.r_probs);
     v->offsets = reinterpret_cast<const int*>(ws + L.offsets);
@@ -811,7 +816,15 @@ moe_status moe_get_workspace_views(const moe_plan* plan, const void* workspace, 
     v->y = reinterpret_cast<const float*>(ws + L.y);
     v->rows_padded = plan->rows_pad;
     v->status = reinterpret_cast<const unsigned*>(ws + L.status);
+    const size_t n = views_bytes < sizeof(known) ? views_bytes : sizeof(known);
+    std::memcpy(views, &known, n);
+    std::memset(static_cast<uint8_t*>(views) + n, 0, views_bytes - n);
     return MOE_OK;
+}
+
+#undef moe_get_workspace_views
+moe_status moe_get_workspace_views(const moe_plan* plan, const void* workspace, moe_workspace_views* v) {
+    return moe_get_workspace_views_sized(plan, workspace, v, kFirstViewsBytes);
 }
 
 moe_status moe_get_device_status(const void* workspace, unsigned* flags_host, void* stream) {

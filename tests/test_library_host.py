@@ -6,6 +6,8 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import shutil
+import subprocess
 
 import pytest
 
@@ -27,6 +29,43 @@ def test_library_exports_every_declared_symbol():
     assert len(names) >= 14, names
     for n in names:
         assert hasattr(lib, n), f"{n} declared in include/moe.h but not exported"
+
+
+def test_views_write_no_more_than_the_callers_struct():
+    """A program built when the struct had fifteen fields gets those; a larger struct is filled as far as
+    the library knows it, the rest zeroed."""
+    lib = ctypes.CDLL(rm.library_path)
+    P, SZ = ctypes.c_void_p, ctypes.c_size_t
+    p = rm.moe_plan_create(hidden=256, ffn=512, num_experts=8, top_k=2, capacity=64, precision="int8")
+    old, sized = lib.moe_get_workspace_views, lib.moe_get_workspace_views_sized
+    old.argtypes, sized.argtypes = [P, P, P], [P, P, P, SZ]
+    word, canary = ctypes.sizeof(P), 0x5A5A5A5A5A5A5A5A
+    ws = 1 << 20  # never dereferenced
+    room = (ctypes.c_uint64 * 24)(*[canary] * 24)
+    assert old(p.handle, ws, room) == 0
+    first = list(room)
+    assert canary not in first[:15] and first[15:] == [canary] * 9
+    for n in (15, 16, 17, 20):
+        room = (ctypes.c_uint64 * 24)(*[canary] * 24)
+        assert sized(p.handle, ws, room, n * word) == 0
+        assert list(room)[:15] == first[:15] and list(room)[n:] == [canary] * (24 - n)
+        assert all(v > ws for v in list(room)[15:min(n, 17)]) and list(room)[17:n] == [0] * max(n - 17, 0)
+    for n in (0, 14 * word, 15 * word + 4):
+        assert sized(p.handle, ws, room, n) == 1
+    assert sized(None, ws, room, 120) == 1 and sized(p.handle, None, room, 120) == 1 and sized(p.handle, ws, None, 120) == 1
+
+
+@pytest.mark.skipif(shutil.which("gcc") is None, reason="needs a C compiler")
+def test_the_header_in_c(tmp_path):
+    """The header as C: a call through the struct of today takes the sized entry point."""
+    src = tmp_path / "views.c"
+    src.write_text('#include "moe.h"\n'
+                   'moe_status f(const moe_plan* p, const void* ws, moe_workspace_views* v) '
+                   '{ return moe_get_workspace_views(p, ws, v); }\n')
+    obj = tmp_path / "views.o"
+    subprocess.check_call(["gcc", "-std=c99", "-Wall", "-Werror", "-pedantic", "-I" + os.path.join(ROOT, "include"), "-c", str(src),
+                           "-o", str(obj)])
+    assert b"moe_get_workspace_views_sized" in obj.read_bytes()
 
 
 def test_version_and_status_strings():
