@@ -341,18 +341,20 @@ PyObject* linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
 }
 
 // exchange capsule, tensor type, parameter type, then the entry points' addresses in the order of
-// Entries; True when this module can serve.
+// Entries; True when this module can serve, False (and no error) when it cannot.
 PyObject* start_module(PyObject*, PyObject* const* v, Py_ssize_t n) {
     constexpr Py_ssize_t kEntries = sizeof(Entries) / sizeof(void*);
     if (n != 3 + kEntries || !PyType_Check(v[1]) || !PyType_Check(v[2])) Py_RETURN_FALSE;
-    const DlExchange* api = static_cast<const DlExchange*>(PyCapsule_GetPointer(v[0], "dlpack_exchange_api"));
-    if (api == nullptr) return nullptr;
+    constexpr const char* kName = "dlpack_exchange_api";
+    if (!PyCapsule_IsValid(v[0], kName)) Py_RETURN_FALSE;  // (sets no error)
+    const DlExchange* api = static_cast<const DlExchange*>(PyCapsule_GetPointer(v[0], kName));
     if (api->major != 1 || api->tensor_from_object == nullptr || api->current_stream == nullptr) Py_RETURN_FALSE;
     uintptr_t at[kEntries];
     for (Py_ssize_t i = 0; i < kEntries; ++i) {
         at[i] = static_cast<uintptr_t>(PyLong_AsUnsignedLongLong(v[3 + i]));
-        if (PyErr_Occurred()) return nullptr;
-        if (at[i] == 0) Py_RETURN_FALSE;
+        const bool wrong = PyErr_Occurred() != nullptr;
+        PyErr_Clear();
+        if (wrong || at[i] == 0) Py_RETURN_FALSE;
     }
     g_lib.get_device = reinterpret_cast<decltype(g_lib.get_device)>(at[0]);
     g_lib.plan_desc = reinterpret_cast<decltype(g_lib.plan_desc)>(at[1]);

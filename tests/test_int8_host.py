@@ -109,3 +109,33 @@ def test_the_compiled_binding_leaves_host_tensors_alone():
         assert rm._short.int8_quantize_rows(*args) is None
     assert rm._short.moe_combine_backward(None, 0, s, s, s, s, s, s, s) is None
     assert rm._short.start(*[None] * 11) is False and rm._short.start() is False
+
+
+def test_a_table_that_the_compiled_binding_does_not_know():
+    """A capsule of another name or no capsule at all: the binding says that it cannot serve and raises
+    nothing, and the library loads without it."""
+    rm.load_library()
+    if rm._short is None:
+        pytest.skip("the compiled binding is not built, or this torch has no exchange table")
+    new = ctypes.pythonapi.PyCapsule_New
+    new.restype, new.argtypes = ctypes.py_object, [ctypes.c_void_p, ctypes.c_char_p, ctypes.c_void_p]
+    room = (ctypes.c_uint64 * 16)()
+    other = new(ctypes.addressof(room), b"some_other_table", None)
+    types = (torch.Tensor, torch.nn.Parameter)
+    for api in (other, 7, None, "dlpack_exchange_api"):
+        assert rm._short.start(api, *types, *[1 << 20] * 8) is False
+    api = torch.Tensor.__dlpack_c_exchange_api__
+    for entries in ([1 << 20] * 7 + [0], [1 << 20] * 7 + [None], [1 << 20] * 7 + [-1], [1 << 20] * 7):
+        assert rm._short.start(api, *types, *entries) is False
+    x, q, s = (torch.zeros(4, 64, dtype=t) for t in (torch.bfloat16, torch.int8, torch.float32))
+    assert rm._short.int8_quantize_rows(None, x, q, s, None) is None  # as before
+
+
+def test_the_library_loads_beside_a_strange_table(monkeypatch):
+    """load_library() with a torch whose exchange attribute is something else falls back to ctypes."""
+    lib = rm.load_library()
+    for api in (object(), 7, "dlpack_exchange_api"):
+        monkeypatch.setattr(torch.Tensor, "__dlpack_c_exchange_api__", api, raising=False)
+        monkeypatch.setattr(rm, "_short", None)
+        rm._load_short(lib)
+        assert rm._short is None
