@@ -57,17 +57,27 @@ def _compile(src, extra, verbose):
 
 def _build_binding(force, verbose):
     src, include = os.path.join(CSRC, "binding.cpp"), sysconfig.get_paths()["include"]
-    if not os.path.exists(os.path.join(include, "Python.h")):
-        print(f"no {include}/Python.h: _binding.so is not built, short calls go through ctypes", file=sys.stderr)
+    if not (force or _stale(BINDING, [src] + _headers() + [__file__])):
         return
-    if force or _stale(BINDING, [src] + _headers() + [__file__]):
+    why = None
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        why = f"no {include}/Python.h"
+    else:
         tmp = BINDING + ".tmp"
         cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-I" + include,
                "-I" + os.path.join(ROOT, "include"), src, "-o", tmp]
         if verbose:
             print(" ".join(cmd), flush=True)
-        subprocess.check_call(cmd)
-        os.replace(tmp, BINDING)
+        try:
+            subprocess.check_call(cmd)
+            os.replace(tmp, BINDING)
+        except (OSError, subprocess.CalledProcessError) as e:
+            why = str(e)
+    if why is not None:
+        # the library does without it; one of other sources must not be loaded beside it
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        print(f"{why}: the compiled binding is not built, short calls go through ctypes", file=sys.stderr)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

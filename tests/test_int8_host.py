@@ -139,3 +139,16 @@ def test_the_library_loads_beside_a_strange_table(monkeypatch):
         monkeypatch.setattr(rm, "_short", None)
         rm._load_short(lib)
         assert rm._short is None
+
+
+@pytest.mark.parametrize("compiler", ["/nowhere/c++", "false"])
+def test_the_library_builds_without_the_binding(tmp_path, monkeypatch, capsys, compiler):
+    """A missing or failing C++ compiler leaves the binding out, an older one too, and says so."""
+    from routed_moe_swiglu_b200 import build
+
+    old = tmp_path / "_binding.so"
+    old.write_bytes(b"of other sources")
+    monkeypatch.setattr(build, "BINDING", str(old))
+    monkeypatch.setenv("CXX", compiler)
+    build._build_binding(True, False)
+    assert list(tmp_path.iterdir()) == [] and "the compiled binding is not built" in capsys.readouterr().err
