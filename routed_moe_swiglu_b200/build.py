@@ -1,5 +1,6 @@
 """Build the CUDA library libroutedmoe.so in-tree with nvcc for sm_100a, and
-_binding.so, the short way from Python into it, with the C++ compiler.
+_binding (for this interpreter), the short way from Python into it, with the
+C++ compiler.
 
     python -m routed_moe_swiglu_b200.build [--force]
 
@@ -17,13 +18,15 @@ import os
 import subprocess
 import sys
 import sysconfig
+from importlib.machinery import EXTENSION_SUFFIXES
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libroutedmoe.so")
-BINDING = os.path.join(PKG, "_binding.so")
+# tagged: it uses the interpreter's full API, and another version must not load it
+BINDING = os.path.join(PKG, "_binding" + EXTENSION_SUFFIXES[0])
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I" + os.path.join(ROOT, "include"),
@@ -57,6 +60,9 @@ def _compile(src, extra, verbose):
 
 def _build_binding(force, verbose):
     src, include = os.path.join(CSRC, "binding.cpp"), sysconfig.get_paths()["include"]
+    untagged = os.path.join(PKG, "_binding.so")  # the name before: any interpreter would load it
+    if os.path.exists(untagged):
+        os.remove(untagged)
     if not (force or _stale(BINDING, [src] + _headers() + [__file__])):
         return
     why = None

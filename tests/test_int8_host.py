@@ -2,6 +2,7 @@
 from __future__ import annotations
 
 import ctypes
+import os
 
 import pytest
 import torch
@@ -152,3 +153,28 @@ def test_the_library_builds_without_the_binding(tmp_path, monkeypatch, capsys, c
     monkeypatch.setenv("CXX", compiler)
     build._build_binding(True, False)
     assert list(tmp_path.iterdir()) == [] and "the compiled binding is not built" in capsys.readouterr().err
+
+
+def test_the_binding_is_built_for_one_interpreter():
+    """The file's name carries this interpreter's tag, so that another Python version does not load it."""
+    from importlib.machinery import EXTENSION_SUFFIXES
+
+    from routed_moe_swiglu_b200 import build
+
+    name = os.path.basename(build.BINDING)
+    assert name == "_binding" + EXTENSION_SUFFIXES[0] != "_binding.so"
+    assert not os.path.exists(os.path.join(build.PKG, "_binding.so"))
+    rm.load_library()
+    if rm._short is not None:
+        assert rm._short.__file__ == build.BINDING
+
+
+def test_an_older_binding_without_a_tag_goes(tmp_path, monkeypatch):
+    from routed_moe_swiglu_b200 import build
+
+    (tmp_path / "_binding.so").write_bytes(b"of some interpreter")
+    monkeypatch.setattr(build, "PKG", str(tmp_path))
+    monkeypatch.setattr(build, "BINDING", str(tmp_path / os.path.basename(build.BINDING)))
+    monkeypatch.setenv("CXX", "false")
+    build._build_binding(False, False)
+    assert list(tmp_path.iterdir()) == []
