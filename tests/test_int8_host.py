@@ -178,3 +178,18 @@ def test_an_older_binding_without_a_tag_goes(tmp_path, monkeypatch):
     monkeypatch.setenv("CXX", "false")
     build._build_binding(False, False)
     assert list(tmp_path.iterdir()) == []
+
+
+def test_the_compiled_binding_serves_where_it_can():
+    """With torch's exchange table, Python.h and a C++ compiler at hand the short way must be there: the
+    tests that go through it skip where it is not."""
+    import shutil
+    import sysconfig
+
+    if getattr(torch.Tensor, "__dlpack_c_exchange_api__", None) is None:
+        pytest.skip("this torch has no exchange table")
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")) or \
+            shutil.which(os.environ.get("CXX", "g++")) is None:
+        pytest.skip("nothing to build it with")
+    rm.load_library()
+    assert rm._short is not None
