@@ -276,6 +276,35 @@ def test_weights_written_just_before():
         _same(out, product_ref(*quantize_ref(x), *quantize_ref(w), False))
 
 
+@pytest.mark.parametrize("rows,K,N", [(17, 2048, 512), (17, 8192, 4096), (100, 4096, 8192), (300, 2048, 512), (700, 2048, 8192)])
+def test_weights_written_just_before_larger_products(rows, K, N):
+    """The same where the product asks for its weights before its rows are quantised: codes of few tokens
+    and wide tiles."""
+    g = torch.Generator(device="cuda").manual_seed(rows + K)
+    x = torch.randn((rows, K), generator=g, device="cuda").to(torch.bfloat16)
+    buf = torch.empty(rm.int8_linear_workspace_bytes(rows, K), dtype=torch.uint8, device="cuda")
+    ws = [torch.randn((N, K), generator=g, device="cuda").to(torch.bfloat16) for _ in range(4)]
+    want = []
+    for w in ws:  # each with codes of its own and a wait between
+        wq, s, out = torch.zeros((N, K), dtype=torch.int8, device="cuda"), torch.zeros(N, device="cuda"), torch.zeros((rows, N), device="cuda")
+        rm.int8_quantize_rows(w, wq, s)
+        torch.cuda.synchronize()
+        rm.int8_linear(x, wq, s, out, buf)
+        torch.cuda.synchronize()
+        want.append(out)
+    wq, s = torch.zeros((N, K), dtype=torch.int8, device="cuda"), torch.zeros(N, device="cuda")
+    outs = [torch.zeros((rows, N), device="cuda") for _ in range(12)]
+    for i, out in enumerate(outs):
+        rm.int8_quantize_rows(ws[i % 4], wq, s)
+        rm.int8_linear(x, wq, s, out, buf)
+    torch.cuda.synchronize()
+    for i, out in enumerate(outs):
+        assert torch.equal(out, want[i % 4]), i
+    pick = torch.arange(0, rows, 16)
+    xc, wc = x[pick.cuda()].cpu(), ws[0][:256].cpu()
+    _same(want[0][pick.cuda(), :256], product_ref(*quantize_ref(xc), *quantize_ref(wc), False))
+
+
 def test_no_rows():
     x, w, ws = torch.zeros(0, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(32, 64, dtype=torch.int8, device="cuda"), \
         torch.ones(32, device="cuda")
