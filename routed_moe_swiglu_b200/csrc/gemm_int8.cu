@@ -38,7 +38,6 @@
 // of weights, 5.8 and 5.2 TB/s of the measured 6.5; a launch's first loads and last
 // tile, ten us together, are what is missing.
 #include "int8.cuh"
-#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -271,8 +270,6 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
-            int last_phase[kStagesMax];
-            for (int s = 0; s < kStagesMax; ++s) last_phase[s] = -1;
             // Experts with one route tile each (decode): every weight tile is read once; its lines go
             // first out of L2, which keeps the rows that the next kernels read there.
             const bool weights_once = kMode != kDense && widest < kRouteTile;
@@ -302,10 +299,7 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
                 for (int t = pair; t < total_tiles && pre < kStages;) {
                     const int2 at = place_of<kMode>(p, num_m, t);
                     const int4 ti = tile_of<kMode>(p, at.x, rows);
-                    if (leader) {
-                        mbar_arrive_expect_tx(&bars->full[pre], stage_bytes(ti.z));
-                        last_phase[pre] = 0;
-                    }
+                    if (leader) mbar_arrive_expect_tx(&bars->full[pre], stage_bytes(ti.z));
                     weights(pre, ti.x, at.y * kPairM + 128 * (int)rank, kb);
                     ++pre;
                     if (++kb == kb_count) {
@@ -336,10 +330,7 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
                             ok = false;
                             break;
                         }
-                        if (leader) {
-                            mbar_arrive_expect_tx(&bars->full[stage], tx);
-                            last_phase[stage] = (int)phase;
-                        }
+                        if (leader) mbar_arrive_expect_tx(&bars->full[stage], tx);
                         weights(stage, ti.x, w_row, kb);
                     }
                     const uint32_t full0 = map_to_cta(smem_u32(&bars->full[stage]), 0);
@@ -358,16 +349,7 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
                     }
                 }
             }
-            if (!ok) {
-                timed_out();
-                if (leader) {  // copies already issued land before shared memory goes away
-                    for (int s = 0; s < kStages; ++s)
-                        if (last_phase[s] >= 0) {
-                            volatile int never = 0;
-                            (void)mbar_wait_bounded(&bars->full[s], (uint32_t)last_phase[s], &never, 100000000ull);
-                        }
-                }
-            }
+            if (!ok) timed_out();  // the MMA issuer then gives up too, and sees the copies land
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -420,7 +402,10 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
                 if (!ok) break;
                 mma_commit_pair_multicast(&bars->acc_full[buf], 0x3);
             }
-            if (!ok) timed_out();
+            if (!ok) {
+                timed_out();
+                int8_fills_land(bars->full, kStages, (int)phase * kStages + stage);  // (parities repeat every 2 n fills)
+            }
             mma_commit_pair(&bars->done);
             volatile int never = 0;
             (void)mbar_wait_bounded(&bars->done, 0, &never, 100000000ull);
@@ -582,7 +567,8 @@ __device__ __forceinline__ void int8_gemm_body(const CUtensorMap& tmA, const Box
         }
     }
 
-    // ---------------- teardown: no pair MMA is in flight once CTA 0 has seen "done"
+    // ---------------- teardown: no pair MMA is in flight once CTA 0 has seen "done", and no copy once
+    // its issuer has used every fill or seen it land
     tc_fence_before_sync();
     __syncthreads();
     cluster_sync();

@@ -22,7 +22,6 @@
 // the end, about a microsecond each.  As two launches of the wide kernels 8.8 us.
 // Sixteen tokens: 7.3 us, their rows' loads side by side (9.0 row after row).
 #include "int8.cuh"
-#include "ptx.cuh"
 
 namespace moe {
 namespace {
@@ -173,14 +172,13 @@ __global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid
     };
 
     float ws[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    int issued = 0, last_phase[4] = {-1, -1, -1, -1};
+    int issued = 0;
     bool ok = true;
     // step i of the slice into its stage: weights, and the tokens' codes (!kFused)
     auto request = [&](int i, bool w, bool b) {
         const int s = i % kStages;
         if (w) {
             mbar_arrive_expect_tx(&sh.full[s], kAAtom + (kFused ? 0u : b_atom));
-            last_phase[s] = (i / kStages) & 1;
             tma_load_2d(sA + s * kAAtom, &tmA, &sh.full[s], (k0 + i) * 128, n0);
         }
         if (b && !kFused)
@@ -268,14 +266,7 @@ __global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid
                 ok = mbar_wait_bounded(&sh.empty[i % kStages], ((i / kStages) & 1) ^ 1, abort_flag, a.wait_limit_ns);
                 if (ok) request(i, true, true);
             }
-            if (!ok) {
-                timed_out();
-                for (int s = 0; s < kStages; ++s)  // copies already issued land before shared memory goes away
-                    if (last_phase[s] >= 0) {
-                        volatile int never = 0;
-                        (void)mbar_wait_bounded(&sh.full[s], (uint32_t)last_phase[s], &never, 100000000ull);
-                    }
-            }
+            if (!ok) timed_out();  // the MMA issuer then gives up too, and sees the copies land
         }
         __syncwarp();
     } else if (warp == 1) {
@@ -283,7 +274,8 @@ __global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid
             const uint64_t a0 = sdesc_kmajor_sw128(smem_u32(sA)), b0 = sdesc_kmajor_sw128(smem_u32(sB));
             const uint32_t idesc = idesc_i8_cta(N);
             if (kFused) ok = mbar_wait_bounded(&sh.b_ready, 0, abort_flag, a.wait_limit_ns);
-            for (int i = 0; i < steps && ok; ++i) {
+            int i = 0;
+            for (; i < steps && ok; ++i) {
                 const int s = i % kStages;
                 ok = mbar_wait_bounded(&sh.full[s], (i / kStages) & 1, abort_flag, a.wait_limit_ns);
                 if (!ok) break;
@@ -295,7 +287,10 @@ __global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid
                     mma_i8_cta(tmem_base, da + kk * 2, db + kk * 2, idesc, (i | kk) != 0 ? 1u : 0u);
                 mma_commit(&sh.empty[s]);
             }
-            if (!ok) timed_out();
+            if (!ok) {
+                timed_out();
+                int8_fills_land(sh.full, kStages, i);
+            }
             mma_commit(&sh.acc_full);
         }
         __syncwarp();
@@ -308,7 +303,11 @@ __global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid
         for (int q = 0; q < 4; ++q) ws[q] = q < left ? __ldg(a.w_scales + n0 + lane * 4 + q) : 0.0f;
         const bool got = __all_sync(0xffffffffu,
                                     mbar_wait_bounded(&sh.acc_full, 0, abort_flag, a.wait_limit_ns));
-        if (!got && lane == 0) timed_out();
+        if (!got && lane == 0) {
+            timed_out();
+            int8_fills_land(&sh.acc_full, 1, 0);  // told to stop by another role: MMAs in flight end before TMEM goes
+        }
+        __syncwarp();
         if (got) {
             tc_fence_after_sync();
             for (int c = 0; c < N; c += 16) {

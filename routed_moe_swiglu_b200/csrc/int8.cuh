@@ -13,6 +13,7 @@
 #pragma once
 
 #include "moe_internal.cuh"
+#include "ptx.cuh"
 
 namespace moe {
 
@@ -152,6 +153,16 @@ __device__ __forceinline__ float sigmoid_approx(float g) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(g * -1.4426950408889634f));
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
     return r;
+}
+
+// The MMA issuer's part of giving up at fill i of its n stages: no copy may land in shared memory that
+// is no longer the kernel's.  Fills i to i + n - 1 are all that can be on their way, as a stage is
+// refilled only once the issuer has used it.  Each gets 0.1 s: one that was asked for lands, one that
+// was not ends the wait (nor does a pair's, if only the other CTA asked: its copies land meanwhile).
+// (Called, not inlined: with the rare path out of the way one token's product takes 0.1 us less.)
+static __device__ __noinline__ void int8_fills_land(uint64_t* full, int n, int i) {
+    volatile int never = 0;
+    for (int j = i; j < i + n; ++j) (void)mbar_wait_bounded(&full[j % n], (uint32_t)(j / n) & 1u, &never, 100000000ull);
 }
 
 struct Int8Gemm {
