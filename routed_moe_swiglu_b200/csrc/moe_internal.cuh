@@ -204,8 +204,21 @@ cudaError_t launch_quantize_rows(const __nv_bfloat16* in, long long rows, int co
 // still running, does its set-up (barriers, TMEM, descriptor prefetch), and
 // waits in pdl_wait() until the predecessor has completed and its writes are
 // visible before reading anything another kernel (or the caller) produced.
-// pdl_trigger() lets the next kernel be scheduled; it changes no ordering
-// of memory, so each kernel issues it first thing.
+// pdl_trigger() lets the next kernel be scheduled.  It orders no memory by
+// itself, so most kernels issue it first thing.  Some must issue it only after
+// their own pdl_wait(), because the kernel behind them reads before its wait
+// what was written before them: it runs only once every block here has
+// triggered, so all that came before this kernel is then done.
+//   kernel that triggers late       kernel behind it, and what it reads early
+//   route_permute_kernel            gather_rows_int8_kernel: live count, x rows
+//   gather_rows_int8_kernel         gate/up int8 (`early`): tiles, sizes, weights
+//   quantize_h_int8_kernel          down int8 (`early`): the same
+//   moe_gemv_int8_kernel, gate/up   the same kernel, down: tiles, weights
+//   int8_quantize_rows_kernel       the dense int8 products in int8_linear
+//                                   (`early`): live count, weights
+//   balance_stats_kernel            balance_finish_kernel: live count
+// Every kernel issues its pdl_wait() before it ends, so that a kernel's end
+// means the end of all before it.
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
