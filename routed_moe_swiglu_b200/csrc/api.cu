@@ -513,67 +513,67 @@ static moe_status forward_impl(const moe_plan* plan, const void* x, const float*
                 : launch_gemm2_int8(tA2, rB2, g, m_tiles * g.n_tiles, s);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
     } else {
-    GemmParams g1{};
-    g1.tiles = tiles;
-    g1.status_words = status;
-    g1.status_flags = status + kStFlags;
-    g1.out = fp4 ? ws + L.hf : ws + L.h;  // NVFP4: fp32 h rows for the per-row quantisation pass
-    g1.out_scales = nullptr;
-    g1.out_ld = plan->fp;  // h rows: F values + zero padding to the down GEMM's K pitch
-    g1.out_cols = (int)plan->fp;  // every padded column: f >= F are zero-weight rows, h = 0
-    g1.a_rows = plan->w1r;  // FC1 weight rows of an expert
-    g1.n_tiles = plan->nt1;
-    g1.k_blocks = plan->ks1;
-    g1.wait_limit_ns = kWaitLimitNs;
-    g1.sfa = wb + plan->wb.w1s;  // MXFP8: A = weights, B = route rows
-    g1.sfb = ws + L.xs;
-    g1.out_scales = fp8 ? ws + L.hs : nullptr;
-    g1.sf_ks_out = plan->ks2;
-    g1.perm = perm;
-    g1.top_k = k;
-    g1.route_probs = probs_in_fc1 ? r_probs : nullptr;
-    g1.clamp = plan->d.gate_up_clamp;
-    g1.relu2 = (plan->d.flags & MOE_FLAG_SQUARED_RELU) != 0;
-    g1.x = static_cast<const uint8_t*>(x);
-    g1.x_pitch = (long long)H * 2;
-    g1.x_bytes = H * 2;
-    g1.xg = ws + L.xq;
-    g1.xg_pitch = plan->hp * 2;
-    g1.ready = ready;
-    g1.copy_next = status + kStCopyNext;
-    g1.tile_started = reinterpret_cast<int*>(status + kStTileStarted);
-    g1.row_scale = fp4 ? reinterpret_cast<const float*>(ws + L.xg) : nullptr;
-    g1.w_scale = fp4 ? reinterpret_cast<const float*>(wb + plan->wb.wg) : nullptr;
-    g1.h_fp32 = fp8 && L.hf != 0 ? reinterpret_cast<float*>(ws + L.hf) : nullptr;
-    if (!mark(3)) return MOE_ERR_CUDA;
-    e = fp8   ? launch_gemm1_mxfp8(tA1, rB1, g1, m_tiles * g1.n_tiles, s)
-        : fp4 ? launch_gemm1_nvfp4(tA1, rB1, g1, m_tiles * g1.n_tiles, s)
-              : launch_gemm1_bf16_pair(tA1, tX, rB1, g1, m_tiles * g1.n_tiles, s);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
-    if (fp4) {  // h rows -> NVFP4 with a scale per row (timed with the gate/up stage)
-        e = launch_quantize_h_nvfp4(reinterpret_cast<const float*>(ws + L.hf), live_count_dev, max_live, k,
-                                    (int)plan->fp, inv, ws + L.h, ws + L.hs, reinterpret_cast<float*>(ws + L.hg),
-                                    status, s);
+        GemmParams g1{};
+        g1.tiles = tiles;
+        g1.status_words = status;
+        g1.status_flags = status + kStFlags;
+        g1.out = fp4 ? ws + L.hf : ws + L.h;  // NVFP4: fp32 h rows for the per-row quantisation pass
+        g1.out_scales = nullptr;
+        g1.out_ld = plan->fp;  // h rows: F values + zero padding to the down GEMM's K pitch
+        g1.out_cols = (int)plan->fp;  // every padded column: f >= F are zero-weight rows, h = 0
+        g1.a_rows = plan->w1r;  // FC1 weight rows of an expert
+        g1.n_tiles = plan->nt1;
+        g1.k_blocks = plan->ks1;
+        g1.wait_limit_ns = kWaitLimitNs;
+        g1.sfa = wb + plan->wb.w1s;  // MXFP8: A = weights, B = route rows
+        g1.sfb = ws + L.xs;
+        g1.out_scales = fp8 ? ws + L.hs : nullptr;
+        g1.sf_ks_out = plan->ks2;
+        g1.perm = perm;
+        g1.top_k = k;
+        g1.route_probs = probs_in_fc1 ? r_probs : nullptr;
+        g1.clamp = plan->d.gate_up_clamp;
+        g1.relu2 = (plan->d.flags & MOE_FLAG_SQUARED_RELU) != 0;
+        g1.x = static_cast<const uint8_t*>(x);
+        g1.x_pitch = (long long)H * 2;
+        g1.x_bytes = H * 2;
+        g1.xg = ws + L.xq;
+        g1.xg_pitch = plan->hp * 2;
+        g1.ready = ready;
+        g1.copy_next = status + kStCopyNext;
+        g1.tile_started = reinterpret_cast<int*>(status + kStTileStarted);
+        g1.row_scale = fp4 ? reinterpret_cast<const float*>(ws + L.xg) : nullptr;
+        g1.w_scale = fp4 ? reinterpret_cast<const float*>(wb + plan->wb.wg) : nullptr;
+        g1.h_fp32 = fp8 && L.hf != 0 ? reinterpret_cast<float*>(ws + L.hf) : nullptr;
+        if (!mark(3)) return MOE_ERR_CUDA;
+        e = fp8   ? launch_gemm1_mxfp8(tA1, rB1, g1, m_tiles * g1.n_tiles, s)
+            : fp4 ? launch_gemm1_nvfp4(tA1, rB1, g1, m_tiles * g1.n_tiles, s)
+                  : launch_gemm1_bf16_pair(tA1, tX, rB1, g1, m_tiles * g1.n_tiles, s);
         if (e != cudaSuccess) return MOE_ERR_CUDA;
-    }
+        if (fp4) {  // h rows -> NVFP4 with a scale per row (timed with the gate/up stage)
+            e = launch_quantize_h_nvfp4(reinterpret_cast<const float*>(ws + L.hf), live_count_dev, max_live, k,
+                                        (int)plan->fp, inv, ws + L.h, ws + L.hs, reinterpret_cast<float*>(ws + L.hg),
+                                        status, s);
+            if (e != cudaSuccess) return MOE_ERR_CUDA;
+        }
 
-    GemmParams g2 = g1;
-    g2.out = ws + L.y;
-    g2.out_ld = H;
-    g2.out_cols = H;
-    g2.n_tiles = plan->nt2;
-    g2.k_blocks = plan->ks2;
-    g2.a_rows = fp8 || fp4 ? H : plan->hr;
-    g2.sfa = wb + plan->wb.w2s;
-    g2.sfb = ws + L.hs;
-    g2.out_scales = nullptr;
-    g2.row_scale = fp4 ? reinterpret_cast<const float*>(ws + L.hg) : nullptr;
-    g2.h_fp32 = nullptr;
-    if (!mark(4)) return MOE_ERR_CUDA;
-    e = fp8   ? launch_gemm2_mxfp8(tA2, rB2, g2, m_tiles * g2.n_tiles, s)
-        : fp4 ? launch_gemm2_nvfp4(tA2, rB2, g2, m_tiles * g2.n_tiles, s)
-              : launch_gemm2_bf16_pair(tA2, rB2, g2, m_tiles * g2.n_tiles, s);
-    if (e != cudaSuccess) return MOE_ERR_CUDA;
+        GemmParams g2 = g1;
+        g2.out = ws + L.y;
+        g2.out_ld = H;
+        g2.out_cols = H;
+        g2.n_tiles = plan->nt2;
+        g2.k_blocks = plan->ks2;
+        g2.a_rows = fp8 || fp4 ? H : plan->hr;
+        g2.sfa = wb + plan->wb.w2s;
+        g2.sfb = ws + L.hs;
+        g2.out_scales = nullptr;
+        g2.row_scale = fp4 ? reinterpret_cast<const float*>(ws + L.hg) : nullptr;
+        g2.h_fp32 = nullptr;
+        if (!mark(4)) return MOE_ERR_CUDA;
+        e = fp8   ? launch_gemm2_mxfp8(tA2, rB2, g2, m_tiles * g2.n_tiles, s)
+            : fp4 ? launch_gemm2_nvfp4(tA2, rB2, g2, m_tiles * g2.n_tiles, s)
+                  : launch_gemm2_bf16_pair(tA2, rB2, g2, m_tiles * g2.n_tiles, s);
+        if (e != cudaSuccess) return MOE_ERR_CUDA;
     }
     if (!mark(5)) return MOE_ERR_CUDA;
 

@@ -87,15 +87,6 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, u
         "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1)
         : "memory");
 }
-__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-}
 __device__ __forceinline__ int4 ld_cluster_v4(uint32_t addr) {
     int4 v;
     asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
@@ -312,7 +303,7 @@ __global__ void __launch_bounds__(kFewThreads) gemm_int8_few_kernel(const __grid
             tc_fence_after_sync();
             for (int c = 0; c < N; c += 16) {
                 uint32_t v[16];
-                tmem_ld_x16(tmem_base + ((uint32_t)(quad * 32) << 16) + c, v);
+                tmem_ld_32x32b_x16(tmem_base + ((uint32_t)(quad * 32) << 16) + c, v);
                 tmem_ld_wait();
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
