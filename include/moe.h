@@ -307,7 +307,10 @@ moe_status moe_balance_loss(const moe_plan* plan, const float* logits, const int
  *     added at column ids[t, j]; routes with an id outside [0, E) are left out of
  *     both sums, and an id that stands twice gets both.
  * Either part may be absent (its pointers NULL), not both.  A token that does not
- * count (lse -infinity) gets a row of zeros; without lse every live token counts.
+ * count (lse -infinity) gets a row of zeros, whatever grad_losses holds; without lse
+ * every live token counts.  The mask thus takes a token out of both parts, as padding
+ * wants it: for a token that only the losses leave out, ask for the two parts in
+ * calls of their own, the chosen part without lse, and add their rows.
  * seq_offsets, num_seqs: as given to moe_balance_loss.  Enqueues work only. */
 moe_status moe_route_backward(const moe_plan* plan, const float* logits, const int* ids, const float* lse,
                               const int* counts, const float* grad_scales, const float* grad_losses,

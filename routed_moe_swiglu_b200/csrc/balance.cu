@@ -26,18 +26,21 @@
 // finishing step adds a sequence's slots in block order: no float atomics, the
 // same bits every run.  The warps of a block share the runs it meets, all at once:
 // long ones in segments, short ones whole.  The rows come through a ring in shared
-// memory that each lane fills for itself (cp.async), two rows ahead.
+// memory that each lane fills for itself (cp.async), two rows ahead (one for more than
+// 512 experts).
 //
-// What bounds it (B200).  Both launches read the logits once and the gradient
-// writes them once; with 65,536 tokens x 128 experts, k 8, 16 sequences (74 MB of
-// memory traffic, 11 us at the copy rate) the losses take 18.3 us, 5.5 of them the
-// finishing kernel, and the gradient 18.6, where a plain copy of the same 34 MB
-// takes 11.8: what is above the copy is instructions (an exponential and eight
-// operations a value, two shuffles a token and route), which register rows and the
-// ring leave in the open when the rows arrive from L2.  Short batches are bound by
-// the chain of launches and meetings: 64 tokens x 8 experts, one cluster and one
-// launch, 6.6 us and the gradient 3.2; 4,099 x 128 in seven sequences 10.6 and 4.5;
-// 3,001 x 1,000 15 and 10.
+// What bounds it (B200).  Both launches read the logits and the gradient writes as
+// much; with 65,536 tokens x 128 experts, k 8, 16 sequences (74 MB from and to memory
+// when the gradient's read of the 34 MB of logits comes from L2, 11 us at the copy
+// rate) the losses take 18.3 us, 5.5 of them the finishing kernel, and the gradient
+// 18.6, where a plain copy of the same 34 MB takes 11.8.  Neither memory (26% and 24%
+// of DRAM's rate in the profile) nor the issue slots (47% and 40%) are full: 16 warps
+// an SM in the sums, 24 in the gradient (103 registers at this width) leave the chain
+// of a row (its arrival, maximum, exponentials, sum) in the open.  Short batches are
+// bound by the chain of launches and meetings, and by the sums' way through memory
+// between them, a lone block's too: 64 tokens x 8 experts, one cluster and one launch,
+// 6.7 us and the gradient 3.2; 4,099 x 128 in seven sequences 10.6 and 4.5; 3,001 x
+// 1,000 15 and 10.
 #include <climits>
 #include <cmath>
 

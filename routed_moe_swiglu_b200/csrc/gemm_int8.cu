@@ -27,13 +27,14 @@
 // Every mbarrier wait is bounded; the pair meets in cluster barriers only at
 // start-up and before TMEM is released.
 //
-// What bounds it (B200).  Dense, 8192^3: 350 us cold and 370-405 sustained, 2.7 to
+// What bounds it (B200).  Dense, 8192^3: 350 us cold and 370-420 sustained, 2.6 to
 // 3.1 POP/s, where twice the measured bf16 rate is 3.3: the power limit lowers the
 // clock.  65,536 routes of 128 experts, H 2,048, F 1,024: gate/up 245 us (2.2
 // POP/s), down 178 us.  Without epilogues they take 210 and 78: gate/up is bound by
 // what an SM takes in from L2 (88 bytes a nanosecond), as its 320 row tiles hold 205
-// rows on average and each loads all of its weights; down by the stores of its fp32
-// y rows, 537 MB, 91 us alone.
+// rows on average and each loads all of its weights; down by all that it moves, 537 MB
+// of fp32 y rows out (91 us alone), 268 MB of weights and 67 MB of codes in, 133 us at
+// the copy rate.
 // 256 tokens of the same experts (16 rows each): 92 us and 51 us for 537 and 268 MB
 // of weights, 5.8 and 5.2 TB/s of the measured 6.5; a launch's first loads and last
 // tile, ten us together, are what is missing.
@@ -183,7 +184,10 @@ __device__ __forceinline__ void store_rows(T* dst, long long ld, const float (&v
     }
 }
 // Arrive on an mbarrier of the cluster without ordering this thread's stores before it: what the
-// arrival says is that the accumulator's loads are done, which tcgen05.wait::ld has waited for.
+// arrival says is that the accumulator's loads are done, which tcgen05.wait::ld has waited for.  The
+// next MMA into it is ordered behind them by the tcgen05 fences on both sides of the barrier, for
+// which the PTX manual's patterns ask an execution order and no more (a relaxed arrival).  Releasing
+// the warp's stores of h or y as well: 65,536 routes 727 us for 710, 777 x 2,688 -> 3,712 17.0 for 16.3.
 __device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t cluster_addr) {
     asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }

@@ -18,8 +18,9 @@
 //
 // One token, six experts of H 2,688, F 1,856 (90 MB of weights, 13.7 us at the
 // copy rate): the whole forward takes 29.2 us, 42.8 on the wide kernels; 13 us of
-// it are five launches' (32.2 with a warp a row where a block's codes are computed).  Eight tokens an expert would
-// cost 96-115 us against 77: hence the limit of four.
+// it are five launches' (32.2 with a warp a row where a block's codes are computed),
+// two of which only put the token's routes in order.  Eight tokens an expert would cost
+// 96-115 us against 77: hence the limit of four.
 #include "int8.cuh"
 
 namespace moe {
